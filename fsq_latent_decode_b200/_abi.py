@@ -31,7 +31,7 @@ EXPORTED = ("fsq_attn_opts_default", "fsq_thresholds", "fsq_encode_pack", "fsq_q
             "fsq_decode_attn_workspace_size", "fsq_decode_attn", "fsq_workspace_status",
             "fsq_status_string", "fsq_format_version", "fsq_decode_attn_noalloc",
             "fsq_decode_attn_noalloc_status", "fsq_decode_attn_multi_workspace_size", "fsq_decode_attn_multi",
-            "fsq_decode_attn_kernel")
+            "fsq_decode_attn_kernel", "fsq_qk_norm_rope", "fsq_cache_evict_workspace_size", "fsq_cache_evict")
 # FSQ_NOALLOC_SCRATCH_BYTES of include/fsq.h (a host test checks the two agree)
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -89,6 +89,14 @@ def _load() -> C.CDLL:
     lib.fsq_decode_attn_noalloc.restype = i32
     lib.fsq_decode_attn_noalloc_status.argtypes = [vp]
     lib.fsq_decode_attn_noalloc_status.restype = i32
+    lib.fsq_qk_norm_rope.argtypes = [vp, i64, i32, vp, vp, i64, vp, i64, i32, vp, vp, i64, i64, i32, vp, i64, f32,
+                                     f32, vp]
+    lib.fsq_qk_norm_rope.restype = i32
+    lib.fsq_cache_evict_workspace_size.argtypes = [i64, i64, i32, i32]
+    lib.fsq_cache_evict_workspace_size.restype = C.c_size_t
+    lib.fsq_cache_evict.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp,
+                                    C.c_size_t, vp]
+    lib.fsq_cache_evict.restype = i32
     lib.fsq_workspace_status.argtypes = [vp, C.c_size_t, vp]
     lib.fsq_workspace_status.restype = i32
     lib.fsq_status_string.argtypes = [i32]
@@ -241,6 +249,20 @@ def decode_attn_noalloc_status(stream=None) -> int:
     return _lib().fsq_decode_attn_noalloc_status(_stream_ptr(stream))
 
 
+def qk_norm_rope_raw(*args) -> int:
+    """fsq_qk_norm_rope with its arguments in order (pointers as integers)."""
+    return _lib().fsq_qk_norm_rope(*args)
+
+
+def cache_evict_workspace_size(B, T, G, levels=16) -> int:
+    return int(_lib().fsq_cache_evict_workspace_size(B, T, G, levels))
+
+
+def cache_evict_raw(*args) -> int:
+    """fsq_cache_evict with its arguments in order (pointers as integers)."""
+    return _lib().fsq_cache_evict(*args)
+
+
 def workspace_status(ws, stream=None) -> int:
     """Reads a device status word: a decode workspace's error word, or an
     append status word (a device tensor of at least 4 bytes).  Blocking."""
@@ -363,6 +385,116 @@ def decode_attn_multi(q, codes, W_kv, T, n_kv, G, code_batch_stride=None, opts=N
                                opts, _ptr(ws), ws.numel(), _ptr(out), _stream_ptr(stream))
     _check(st, "fsq_decode_attn_multi")
     return out
+
+
+def _opt_ptr(t):
+    return None if t is None else int(t.data_ptr())
+
+
+def _heads(t, what):
+    """Token stride of a [n_tok, heads, d_h] tensor whose heads lie d_h apart (any token stride)."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what} must be [n_tok, heads, d_h] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _of_type(t, dtype, what):
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+
+
+def _on_current_device(what, *tensors):
+    """The calls launch on the current device: refuse tensors that live elsewhere."""
+    import torch
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
+
+
+def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, eps=1e-6, rope_base=1.0e6,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of every query (and key) head, then its rotary position, in one
+    pass: q [n_tok, n_q, 128] and optionally k [n_tok, n_k, 128] bf16, views of a
+    fused projection included; token t is at pos0 + positions[t] (int32; None:
+    0, 1, ..).  A decode step passes positions=seq_lens and pos0=-1.  Returns
+    q_out, or (q_out, k_out) when k is given; an output may be its own input."""
+    import torch
+    n_tok, n_q, d_h = q.shape
+    for t, what in ((q, "q"), (k, "k"), (q_gain, "q_gain"), (k_gain, "k_gain"), (q_out, "q_out"), (k_out, "k_out")):
+        _of_type(t, torch.bfloat16, what)
+    _of_type(positions, torch.int32, "positions")
+    if k is not None and (k.shape[0] != n_tok or k.shape[2] != d_h):
+        raise ValueError("k must be [n_tok, n_k, d_h] of the same tokens as q")
+    for t, n, what in ((positions, n_tok, "positions"), (q_gain, d_h, "q_gain"), (k_gain, d_h, "k_gain")):
+        if t is not None and (t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{what} must hold {n} contiguous values")
+    if q_out is None:
+        q_out = torch.empty((n_tok, n_q, d_h), dtype=torch.bfloat16, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("an output must have its input's shape")
+    n_k = 0 if k is None else k.shape[1]
+    ld = [_heads(q, "q"), _heads(q_out, "q_out"), _heads(k, "k") if n_k else 0, _heads(k_out, "k_out") if n_k else 0]
+    _on_current_device("qk_norm_rope", q, k, q_gain, k_gain, positions, q_out, k_out)
+    st = qk_norm_rope_raw(_ptr(q), ld[0], n_q, _opt_ptr(q_gain), _ptr(q_out), ld[1], _opt_ptr(k), ld[2], n_k,
+                          _opt_ptr(k_gain), _opt_ptr(k_out), ld[3], n_tok, d_h, _opt_ptr(positions), int(pos0),
+                          float(eps), float(rope_base), _stream_ptr(stream))
+    _check(st, "fsq_qk_norm_rope")
+    return q_out if k is None else (q_out, k_out)
+
+
+def _cache_stride(codes, rb, T, what):
+    """Batch stride in bytes of a [B, T_max, R] uint8 cache with contiguous rows."""
+    if codes.dim() != 3 or codes.shape[2] != rb or codes.shape[1] < T or codes.stride(2) != 1 or \
+            (codes.shape[1] > 1 and codes.stride(1) != rb):
+        raise ValueError(f"{what} must be [B, T_max >= {T}, {rb}] uint8 with contiguous rows")
+    # a size-1 leading dim may carry any stride
+    return codes.stride(0) if codes.shape[0] > 1 else (codes.shape[1] * rb + 15) // 16 * 16
+
+
+def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=None, out=None, acc_out=None,
+                lens_out=None, kept=None, workspace=None, stream=None):
+    """Keeps each row's last n_recent tokens and the heaviest of the others,
+    n_keep in all, packed in order to the front: of codes [B, T_max, R] and
+    acc [B, T_max'] fp32 themselves (out is None), or into out / acc_out.  Row b
+    holds T tokens, or seq_lens[b].  lens_out [B] int32 receives the new lengths
+    (it may be seq_lens), kept [B, n_keep] int32 the old indices (-1 behind the
+    last).  Returns (codes, acc) as written."""
+    import torch
+    B = codes.shape[0]
+    rb = row_bytes(G, levels)
+    _of_type(codes, torch.uint8, "codes")
+    _of_type(acc, torch.float32, "acc")
+    if (out is None) != (acc_out is None):
+        raise ValueError("out and acc_out go together")
+    if out is None:
+        out, acc_out = codes, acc
+    _of_type(out, torch.uint8, "out")
+    _of_type(acc_out, torch.float32, "acc_out")
+    n_out = T if out is codes else min(T, n_keep)
+    strides = []
+    for t, n, what in ((acc, T, "acc"), (acc_out, n_out, "acc_out")):
+        if t.dim() != 2 or t.shape[0] != B or t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what} must be [B, at least {n}] with contiguous rows")
+        strides.append(t.stride(0) if B > 1 else max(t.stride(0), t.shape[1]))
+    if out.shape[0] != B:
+        raise ValueError("out must hold the rows of codes")
+    for t, shape, what in ((seq_lens, (B,), "seq_lens"), (lens_out, (B,), "lens_out"), (kept, (B, n_keep), "kept")):
+        _of_type(t, torch.int32, what)
+        if t is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous {shape}")
+    nbytes = cache_evict_workspace_size(B, T, G, levels)
+    if nbytes == 0:
+        raise FsqError(FSQ_ERR_INVALID_ARG, "fsq_cache_evict_workspace_size")
+    cs, os_ = _cache_stride(codes, rb, T, "codes"), _cache_stride(out, rb, n_out, "out")
+    _on_current_device("cache_evict", codes, acc, out, acc_out, seq_lens, lens_out, kept)
+    ws = (workspace or Workspace(codes.device)).get(nbytes)
+    st = cache_evict_raw(_ptr(codes), cs, _ptr(acc), strides[0], _opt_ptr(seq_lens), B, T, n_keep, n_recent, G, levels,
+                         _ptr(out), os_, _ptr(acc_out), strides[1], _opt_ptr(lens_out), _opt_ptr(kept), _ptr(ws),
+                         ws.numel(), _stream_ptr(stream))
+    _check(st, "fsq_cache_evict")
+    return out, acc_out
 
 
 def default_scale(d_h: int) -> float:

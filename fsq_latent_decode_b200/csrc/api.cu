@@ -50,6 +50,15 @@ cudaError_t launch_absorbed_tc(const uint16_t *q, const uint8_t *codes, int64_t 
                                const uint16_t *W_kv, float scale, int S, int64_t tps, uint8_t *qphys, float *corr,
                                float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32,
                                uint32_t stall_ns, void *const *prof, cudaStream_t st);
+cudaError_t launch_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,
+                             int64_t ldqo, const uint16_t *k, int64_t ldk, int n_k, const uint16_t *k_gain,
+                             uint16_t *k_out, int64_t ldko, int64_t n_tok, const int32_t *positions, int64_t pos0,
+                             float eps, float rope_base, cudaStream_t st);
+size_t evict_workspace_bytes(int64_t B, int64_t T, int R);
+cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc, int64_t acc_stride,
+                         const int32_t *lens, int64_t B, int64_t T, int64_t n_keep, int64_t n_recent, int R,
+                         uint8_t *out, int64_t ostride, float *acc_out, int64_t acc_ostride, int32_t *lens_out,
+                         int32_t *kept, uint8_t *ws, cudaStream_t st);
 
 namespace {
 
@@ -60,6 +69,12 @@ constexpr bool kEnableTc = true;  // tensor-core absorbed kernel (being validate
 constexpr size_t kMaxDynSmem = 227 * 1024;  // dynamic shared memory a CTA may request
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
 
 // Level count of a levels field (0 selects 16); 0 when unsupported.
 int levels_of(int levels) {
@@ -371,6 +386,83 @@ fsq_status fsq_decode_attn_multi(const uint16_t *q, int64_t B, int n_new, int n_
                            err, o, op.out_fp32, op.prof_events, s);
   }
   return from_cuda(e);
+}
+
+fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,
+                            int64_t ldq_out, const uint16_t *k, int64_t ldk, int n_k, const uint16_t *k_gain,
+                            uint16_t *k_out, int64_t ldk_out, int64_t n_tok, int d_h, const int32_t *positions,
+                            int64_t pos0, float eps, float rope_base, fsq_stream_t stream) {
+  if (n_tok < 0 || n_q < 1 || n_k < 0 || d_h < 1) return FSQ_ERR_INVALID_ARG;
+  if (d_h != FSQ_HEAD_DIM || (int64_t)n_q + n_k > kMaxGridRows || n_tok > INT32_MAX) return FSQ_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f) || !(rope_base > 1.f) || isinf(eps) || isinf(rope_base)) return FSQ_ERR_INVALID_ARG;
+  if (n_tok == 0) return FSQ_OK;
+  const int64_t wq = (int64_t)n_q * d_h, wk = (int64_t)n_k * d_h;
+  if (!q || !q_out || (n_k && (!k || !k_out))) return FSQ_ERR_INVALID_ARG;
+  if (n_tok > 1 && (ldq < wq || ldq_out < wq || (n_k && (ldk < wk || ldk_out < wk)))) return FSQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || ldq % 8 || ldq_out % 8) return FSQ_ERR_MISALIGNED;
+  if (n_k && (!aligned16(k) || !aligned16(k_out) || ldk % 8 || ldk_out % 8)) return FSQ_ERR_MISALIGNED;
+  if (!aligned16(q_gain) || (n_k && !aligned16(k_gain)) || ((uintptr_t)positions & 3u)) return FSQ_ERR_MISALIGNED;
+  // two tensors of interleaved heads (one projection's q and k) span the same
+  // bytes without sharing any, so spans are only told apart within a token
+  const bool q_same = q_out == q && (ldq_out == ldq || n_tok == 1), k_same = k_out == k && (ldk_out == ldk || n_tok == 1);
+  auto clash = [&](const uint16_t *a, int64_t lda, int64_t wa, const uint16_t *b, int64_t ldb, int64_t wb) {
+    const int64_t na = ((n_tok - 1) * lda + wa) * 2, nb = ((n_tok - 1) * ldb + wb) * 2;
+    if (!overlap(a, na, b, nb)) return false;
+    if (lda != ldb || n_tok == 1) return true;
+    // equal strides: token rows meet if the offset between them, modulo the stride, is within a row
+    int64_t d = (int64_t)(((intptr_t)b - (intptr_t)a) / 2) % lda;
+    if (d < 0) d += lda;
+    return d < wa || lda - d < wb;
+  };
+  if (!q_same && clash(q, ldq, wq, q_out, ldq_out, wq)) return FSQ_ERR_INVALID_ARG;
+  if (n_k) {
+    if (!k_same && clash(k, ldk, wk, k_out, ldk_out, wk)) return FSQ_ERR_INVALID_ARG;
+    if (clash(q, ldq, wq, k_out, ldk_out, wk) || clash(k, ldk, wk, q_out, ldq_out, wq) ||
+        clash(q_out, ldq_out, wq, k_out, ldk_out, wk))
+      return FSQ_ERR_INVALID_ARG;
+  }
+  return from_cuda(launch_norm_rope(q, ldq, n_q, q_gain, q_out, ldq_out, k, ldk, n_k, k_gain, k_out, ldk_out, n_tok,
+                                    positions, pos0, eps, rope_base, (cudaStream_t)stream));
+}
+
+size_t fsq_cache_evict_workspace_size(int64_t B, int64_t T, int G, int levels) {
+  const int L = levels_of(levels);
+  if (B < 0 || T < 0 || T > INT32_MAX || !L || !width_ok(G, L)) return 0;
+  if (B > 0 && (T + 31) / 32 > INT32_MAX / B) return 0;
+  return evict_workspace_bytes(B, T, G * bits_of_levels(L) / 8);
+}
+
+fsq_status fsq_cache_evict(const uint8_t *codes, int64_t code_batch_stride_bytes, const float *acc,
+                           int64_t acc_stride, const int32_t *seq_lens, int64_t B, int64_t T, int64_t n_keep,
+                           int64_t n_recent, int G, int levels, uint8_t *codes_out, int64_t out_stride_bytes,
+                           float *acc_out, int64_t acc_out_stride, int32_t *lens_out, int32_t *kept, void *workspace,
+                           size_t workspace_bytes, fsq_stream_t stream) {
+  if (B < 0 || T < 0 || n_keep < 1 || n_recent < 0 || n_recent > n_keep || G < 2) return FSQ_ERR_INVALID_ARG;
+  const int L = levels_of(levels);
+  if (!L || !width_ok(G, L) || T > INT32_MAX || n_keep > INT32_MAX) return FSQ_ERR_UNSUPPORTED;
+  if (B > 0 && (T + 31) / 32 > INT32_MAX / B) return FSQ_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return FSQ_OK;
+  if (!codes || !acc || !codes_out || !acc_out) return FSQ_ERR_INVALID_ARG;
+  const int64_t R = (int64_t)G * bits_of_levels(L) / 8, rows_out = T < n_keep ? T : n_keep;
+  if (code_batch_stride_bytes < T * R || acc_stride < T) return FSQ_ERR_INVALID_ARG;
+  if (out_stride_bytes < rows_out * R || acc_out_stride < rows_out) return FSQ_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(codes_out) || code_batch_stride_bytes % 16 || out_stride_bytes % 16)
+    return FSQ_ERR_MISALIGNED;
+  if (((uintptr_t)acc | (uintptr_t)acc_out | (uintptr_t)seq_lens | (uintptr_t)lens_out | (uintptr_t)kept) & 3u)
+    return FSQ_ERR_MISALIGNED;
+  const bool in_place = codes == codes_out;
+  if (in_place != (acc == acc_out)) return FSQ_ERR_INVALID_ARG;
+  if (in_place && (code_batch_stride_bytes != out_stride_bytes || acc_stride != acc_out_stride))
+    return FSQ_ERR_INVALID_ARG;
+  if (!in_place &&
+      (overlap(codes, (B - 1) * code_batch_stride_bytes + T * R, codes_out, (B - 1) * out_stride_bytes + rows_out * R) ||
+       overlap(acc, ((B - 1) * acc_stride + T) * 4, acc_out, ((B - 1) * acc_out_stride + rows_out) * 4)))
+    return FSQ_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < evict_workspace_bytes(B, T, (int)R)) return FSQ_ERR_WORKSPACE;
+  if ((uintptr_t)workspace & 255u) return FSQ_ERR_MISALIGNED;
+  return from_cuda(launch_evict(codes, code_batch_stride_bytes, acc, acc_stride, seq_lens, B, T, n_keep, n_recent,
+                                (int)R, codes_out, out_stride_bytes, acc_out, acc_out_stride, lens_out, kept,
+                                (uint8_t *)workspace, (cudaStream_t)stream));
 }
 
 fsq_status fsq_workspace_status(const void *workspace, size_t workspace_bytes, fsq_stream_t stream) {

@@ -1,0 +1,489 @@
+// Eviction from the code cache by accumulated attention weight.
+//
+// Row b holds L_b tokens with weights acc[b][t].  It keeps its last n_recent
+// tokens and, of the others, the n_keep - n_recent with the largest weight
+// (equal weights: the lowest index first); the kept rows move to the front of
+// the row in their order.  Rows of at most n_keep tokens keep everything.
+//
+// Two kernels:
+//  evict_select   one thread-block cluster per row finds the weight of the last
+//                 token that stays, by a radix select over order-preserving
+//                 32-bit keys (digits of 11, 11 and 10 bits: histograms in
+//                 shared memory, each CTA of the cluster adds up a slice of the
+//                 bins over all of them), then writes one keep bit per token
+//                 and each chunk's position in the packed row.
+//  evict_compact  one CTA per chunk of tokens copies its kept rows, weights and
+//                 indices to their places.
+//
+// Bound by memory: 4 bytes of weight per token, twice the code bytes of every
+// kept token.  In place, a chunk's destination lies at or before its source,
+// in the sources of at most two earlier chunks: a chunk loads its kept rows
+// into registers or shared memory, publishes that it has, waits until the
+// chunks it overwrites have published the same, and stores.  Chunks are taken in
+// ascending order from a counter, and a chunk publishes before it waits, so the
+// chunks waited for are always running or done: the wait ends whatever the
+// scheduling.  It is bounded all the same (FSQ_ERR_TIMEOUT).
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace fsq {
+namespace evict {
+
+constexpr int kNT = 1024;              // threads of a select CTA
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;
+constexpr int kPieceTok = kNT;         // tokens a select CTA looks at in one step
+constexpr int kCopyNT = 256;           // threads of a compaction CTA
+constexpr int kCopyBytes = 32 * 1024;  // code bytes of a chunk
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+// Tokens per chunk: a power of two of at least 32 tokens (whole keep words, and
+// a chunk's first row 16-byte aligned) with at most kCopyBytes of codes, or 32.
+__host__ __device__ inline int chunk_tokens(int R) {
+  int c = 1024;
+  while (c > 32 && c * R > kCopyBytes) c >>= 1;
+  return c;
+}
+
+struct Plan {
+  int R, chunk;
+  int64_t nchunk, words;  // per row
+  size_t off_rows, off_bits, off_off, off_flag, off_ticket, total;
+};
+inline Plan plan_of(int64_t B, int64_t T, int R) {
+  Plan p;
+  p.R = R;
+  p.chunk = chunk_tokens(R);
+  p.nchunk = (T + p.chunk - 1) / p.chunk;
+  p.words = p.nchunk * (p.chunk / 32);
+  size_t off = kWsHeader;
+  p.off_rows = off;  // per row: length before, length after, whether the given length was out of range
+  off = align_up(off + 3 * sizeof(int32_t) * (size_t)B, 256);
+  p.off_bits = off;
+  off = align_up(off + sizeof(uint32_t) * (size_t)(B * p.words), 256);
+  p.off_off = off;
+  off = align_up(off + sizeof(int32_t) * (size_t)(B * p.nchunk), 256);
+  p.off_flag = off;
+  off = align_up(off + sizeof(uint32_t) * (size_t)(B * p.nchunk), 256);
+  p.off_ticket = off;
+  off = align_up(off + sizeof(uint32_t), 256);
+  p.total = off;
+  return p;
+}
+
+// Order-preserving key: larger weight, larger key; -0 equals +0; NaN is below
+// every number.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  if (v != v) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+struct SelectParams {
+  const float *acc;
+  int64_t acc_stride;
+  const int32_t *lens;
+  int64_t T, n_keep, n_recent;
+  int32_t *rows;    // [B][3]
+  uint32_t *bits;   // [B][words]
+  int32_t *off;     // [B][nchunk]
+  uint32_t *flag;   // [B][nchunk]
+  uint32_t *ticket;
+  uint32_t *err;
+  int32_t *lens_out, *kept;
+  int64_t nchunk, words;
+  int chunk;
+};
+
+// Exclusive prefix of `v` over the CTA's threads; *total: the sum.  red has
+// kNT / 32 entries; two barriers.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint32_t *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t n = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += n;
+  }
+  if (lane == 31) red[warp] = s;
+  __syncthreads();
+  uint32_t w = red[lane];  // kNT / 32 == 32 warps
+  uint32_t ws = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t n = __shfl_up_sync(0xffffffffu, ws, o);
+    if (lane >= o) ws += n;
+  }
+  *total = __shfl_sync(0xffffffffu, ws, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, ws - w, warp);
+  __syncthreads();
+  return before + s - v;
+}
+
+__global__ void __launch_bounds__(kNT) evict_select(SelectParams p) {
+  static_assert(kNT / 32 == 32, "block_prefix reads one warp total per lane");
+  cg::cluster_group cl = cg::this_cluster();
+  const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  __shared__ uint32_t hist[kBins];    // this CTA's keys by digit
+  __shared__ uint32_t slice[kMaxCluster];   // per rank: its slice's keys, all CTAs (written by the ranks)
+  __shared__ uint32_t found[2];       // digit and keys still to keep inside it (written by the rank that finds it)
+  __shared__ uint32_t total[kMaxCluster];   // per rank: kept tokens / ties of its segment
+  __shared__ uint32_t red[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t b = blockIdx.x / CS;
+  pdl_wait();
+  const int64_t L = p.lens ? [&]() -> int64_t {
+    const int64_t v = p.lens[b];
+    return v < 0 ? 0 : (v > p.T ? p.T : v);
+  }() : p.T;
+  const bool bad = p.lens && p.lens[b] != L;
+  const int64_t after = min(L, p.n_keep);
+  // this CTA's tokens: whole steps, so that they are whole keep words; chunks
+  // are at most one step wide and divide it
+  const int64_t steps = (p.T + kPieceTok - 1) / kPieceTok, per = (steps + CS - 1) / CS;
+  const int64_t s0 = min((int64_t)rank * per * kPieceTok, p.T), s1 = min(s0 + per * kPieceTok, p.T);
+  const float *acc = p.acc + b * p.acc_stride;
+  const int64_t c0 = s0 / p.chunk, c1 = s0 < s1 ? (s1 + p.chunk - 1) / p.chunk : c0;  // and its chunks
+  for (int64_t c = c0 + tid; c < c1; c += kNT) p.flag[b * p.nchunk + c] = 0u;
+  if (blockIdx.x == 0 && tid == 0) {
+    *p.ticket = 0u;
+    *p.err = 0u;
+  }
+  const int64_t N = L - p.n_recent;               // candidates (when the row is cut at all)
+  uint32_t need = 0;                              // candidates to keep
+  uint32_t limit = 0;                             // key of the last one
+  uint32_t ties = 0;                              // of the keys equal to it, how many stay
+  const bool cut = L > p.n_keep;
+  if (cut) need = (uint32_t)(p.n_keep - p.n_recent);
+  if (cut && need > 0) {
+    const int64_t e1 = min(s1, N);
+    int shift = 32;
+    uint32_t high = 0;                            // digits found so far, in place
+    ties = need;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bitsn = pass < 2 ? 11 : 10;
+      const int bins = 1 << bitsn;
+      const uint32_t above = shift == 32 ? 0u : (0xFFFFFFFFu << shift);
+      shift -= bitsn;
+      for (int i = tid; i < bins; i += kNT) hist[i] = 0u;
+      __syncthreads();
+      for (int64_t t = s0 + tid; t < e1; t += kNT) {
+        const uint32_t k = key_of(acc[t]);
+        if ((k & above) == high) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      }
+      cl.sync();
+      // rank r adds up bins [r, r + 1) * bins / CS over the cluster (bins / CS <= 2 kNT)
+      const int sb = bins / CS, b0 = rank * sb;
+      uint32_t mine[2] = {0u, 0u};                // bins 2 tid, 2 tid + 1 of the slice, counted from its top
+      const int hi = b0 + sb - 1;
+      for (int r = 0; r < CS; ++r) {
+        const uint32_t *h = cl.map_shared_rank(hist, r);
+        if (2 * tid < sb) mine[0] += h[hi - 2 * tid];
+        if (2 * tid + 1 < sb) mine[1] += h[hi - 2 * tid - 1];
+      }
+      uint32_t sum;
+      const uint32_t before = block_prefix(mine[0] + mine[1], red, &sum);
+      if (tid < CS) cl.map_shared_rank(slice, tid)[rank] = sum;
+      cl.sync();
+      uint32_t higher = 0;                        // keys in the slices above this one
+      for (int r = rank + 1; r < CS; ++r) higher += slice[r];
+      const uint32_t n0 = higher + before, n1 = n0 + mine[0], n2 = n1 + mine[1];
+      const int at = (n0 < ties && ties <= n1) ? 0 : (n1 < ties && ties <= n2) ? 1 : -1;
+      if (at >= 0) {                              // one thread of the cluster
+        const uint32_t digit = (uint32_t)(hi - 2 * tid - at), left = ties - (at ? n1 : n0);
+        for (int r = 0; r < CS; ++r) {
+          uint32_t *f = cl.map_shared_rank(found, r);
+          f[0] = digit;
+          f[1] = left;
+        }
+      }
+      cl.sync();
+      high |= found[0] << shift;
+      ties = found[1];
+    }
+    limit = high;
+  }
+  // keep bits: above the limit, or equal to it and among the first `ties`; the recent tokens
+  auto state = [&](int64_t t) -> int {            // 0 goes, 1 stays, 2 stays if its turn among the ties comes
+    if (t >= L) return 0;
+    if (!cut || t >= N) return 1;
+    if (need == 0) return 0;
+    const uint32_t k = key_of(acc[t]);
+    return k > limit ? 1 : k == limit ? 2 : 0;
+  };
+  uint32_t eq_before = 0;                         // ties in the segments before this one
+  if (cut && need > 0) {
+    uint32_t eq = 0;
+    for (int64_t t = s0 + tid; t < min(s1, N); t += kNT) eq += key_of(acc[t]) == limit ? 1u : 0u;
+    uint32_t sum;
+    block_prefix(eq, red, &sum);
+    if (tid < CS) cl.map_shared_rank(total, tid)[rank] = sum;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) eq_before += total[r];
+    cl.sync();
+  }
+  // first pass over the segment: keep words and this segment's kept tokens before each chunk
+  uint32_t run = 0;
+  for (int64_t base = s0; base < s1; base += kPieceTok) {
+    const int64_t t = base + tid;
+    const int st = t < s1 ? state(t) : 0;
+    bool keep = st == 1;
+    if (cut && need > 0) {
+      uint32_t sum;
+      const uint32_t eq = block_prefix(st == 2 ? 1u : 0u, red, &sum);
+      keep = keep || (st == 2 && eq_before + eq < ties);
+      eq_before += sum;
+    }
+    const uint32_t word = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0 && t < p.words * 32) p.bits[b * p.words + t / 32] = word;
+    uint32_t sum;
+    const uint32_t pre = block_prefix(keep ? 1u : 0u, red, &sum);
+    if (tid % p.chunk == 0 && t < s1) p.off[b * p.nchunk + t / p.chunk] = (int32_t)(run + pre);
+    run += sum;
+  }
+  if (tid < CS) cl.map_shared_rank(total, tid)[rank] = run;
+  cl.sync();
+  uint32_t before = 0;
+  for (int r = 0; r < rank; ++r) before += total[r];
+  for (int64_t c = c0 + tid; c < c1; c += kNT) p.off[b * p.nchunk + c] += (int32_t)before;
+  // every CTA of the cluster has read lens[b], which lens_out may alias
+  if (rank == 0 && tid == 0) {
+    p.rows[3 * b] = (int32_t)L;
+    p.rows[3 * b + 1] = (int32_t)after;
+    p.rows[3 * b + 2] = bad ? 1 : 0;
+    if (p.lens_out) p.lens_out[b] = (int32_t)after;
+  }
+  if (p.kept)
+    for (int64_t i = after + (int64_t)rank * kNT + tid; i < p.n_keep; i += (int64_t)CS * kNT) p.kept[b * p.n_keep + i] = -1;
+  cl.sync();  // no CTA leaves while another may still write its shared memory
+}
+
+struct CopyParams {
+  const uint8_t *codes;
+  uint8_t *out;
+  int64_t bstride, ostride;
+  const float *acc;
+  float *acc_out;
+  int64_t acc_stride, acc_ostride;
+  int32_t *kept;
+  const int32_t *rows;
+  const uint32_t *bits;
+  const int32_t *off;
+  uint32_t *flag, *ticket, *err;
+  int64_t B, n_keep, nchunk, words;
+  int R, chunk, in_place;
+};
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// U: bytes that are moved at once (the largest power of two up to 16 dividing
+// a row).  Rows of whole 16-byte pieces are loaded one by one, only the kept
+// ones, into registers; others come with their whole chunk into shared memory
+// (aligned, contiguous loads), and the packed bytes are put together there.
+template <int U>
+__global__ void __launch_bounds__(kCopyNT) evict_compact(CopyParams p) {
+  extern __shared__ __align__(16) uint8_t stage[];  // U < 16: the chunk's code bytes
+  __shared__ uint16_t list[1024];                   // kept tokens of the chunk
+  __shared__ uint32_t wcnt[32];
+  __shared__ uint32_t order;
+  __shared__ int go;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  int64_t job = blockIdx.x;
+  if (p.in_place) {
+    if (tid == 0) order = atomicAdd(p.ticket, 1u);
+    __syncthreads();
+    job = order;
+  }
+  // rows side by side, chunks ascending
+  const int64_t b = job % p.B, c = job / p.B;
+  const int64_t L = p.rows[3 * b], after = p.rows[3 * b + 1];
+  if (c == 0 && tid == 0 && p.rows[3 * b + 2]) record_error(p.err, FSQ_ERR_INVALID_ARG);  // the word is clear by now
+  const int64_t t0 = c * p.chunk;
+  if (t0 >= L) return;  // nothing here; nobody waits for a chunk behind the last token
+  const bool still = p.in_place && L == after;  // nothing moves
+  const int64_t dst = p.off[b * p.nchunk + c];
+  // the chunk's kept tokens, ascending
+  const uint32_t *bits = p.bits + b * p.words + t0 / 32;
+  const int nw = p.chunk / 32;
+  if (tid < 32) {
+    const uint32_t n = tid < nw ? __popc(bits[tid]) : 0u;
+    uint32_t s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, s, o);
+      if (tid >= o) s += v;
+    }
+    wcnt[tid] = s;
+  }
+  __syncthreads();
+  for (int t = tid; t < p.chunk; t += kCopyNT) {
+    const uint32_t w = bits[t / 32];
+    if ((w >> (t % 32)) & 1u)
+      list[(t >= 32 ? wcnt[t / 32 - 1] : 0u) + __popc(w & ((1u << (t % 32)) - 1u))] = (uint16_t)t;
+  }
+  __syncthreads();
+  const int n = (int)wcnt[nw - 1];
+  const float *acc = p.acc + b * p.acc_stride + t0;
+  if (p.kept)
+    for (int i = tid; i < n; i += kCopyNT) p.kept[b * p.n_keep + dst + i] = (int32_t)(t0 + list[i]);
+  if (still) return;
+  // ---- load
+  constexpr int kRegs = kCopyBytes / 16 / kCopyNT;  // 16-byte pieces of a thread
+  const uint8_t *src = p.codes + b * p.bstride + t0 * p.R;
+  const int rows_here = (int)min((int64_t)p.chunk, L - t0);
+  float av[4];  // chunk <= 4 kCopyNT
+#pragma unroll
+  for (int k = 0; k < 4; ++k) av[k] = tid + k * kCopyNT < n ? acc[list[tid + k * kCopyNT]] : 0.f;
+  uint4 v[U == 16 ? kRegs : 1];
+  const int ppr = p.R / U;          // pieces per row
+  if constexpr (U == 16) {
+#pragma unroll
+    for (int k = 0; k < kRegs; ++k) {
+      const int i = tid + k * kCopyNT;
+      if (i < n * ppr) v[k] = *reinterpret_cast<const uint4 *>(src + (int64_t)list[i / ppr] * p.R + (i % ppr) * 16);
+    }
+  } else {
+    const int nb = rows_here * p.R;  // the row's bytes may end inside a 16-byte piece
+    for (int i = tid; i < nb / 16; i += kCopyNT)
+      *reinterpret_cast<uint4 *>(stage + 16 * i) = *reinterpret_cast<const uint4 *>(src + 16 * i);
+    for (int i = nb / 16 * 16 + tid; i < nb; i += kCopyNT) stage[i] = src[i];
+  }
+  if (tid == 0) go = 1;
+  __syncthreads();
+  if (p.in_place) {
+    // publish that this chunk is loaded, then wait for the chunks its destination covers
+    if (tid == 0) {
+      __threadfence();
+      uint32_t *flag = p.flag + b * p.nchunk;
+      store_release(flag + c, 1u);
+      if (n > 0) {
+        const uint64_t start = ptx::globaltimer_ns();
+        for (int64_t d = dst / p.chunk; d <= (dst + n - 1) / p.chunk && d < c && go; ++d)
+          while (load_acquire(flag + d) == 0u)
+            if (ptx::globaltimer_ns() - start > kWaitNs) {
+              record_error(p.err, FSQ_ERR_TIMEOUT);
+              go = 0;
+              break;
+            }
+      }
+    }
+    __syncthreads();
+    if (!go) return;
+  }
+  // ---- store
+  uint8_t *to = p.out + b * p.ostride + dst * p.R;
+  if constexpr (U == 16) {
+#pragma unroll
+    for (int k = 0; k < kRegs; ++k) {
+      const int i = tid + k * kCopyNT;
+      if (i < n * ppr) *reinterpret_cast<uint4 *>(to + (int64_t)i * 16) = v[k];
+    }
+  } else {
+    // whole aligned 16-byte pieces of the destination, and the bytes at both ends
+    const int nb = n * p.R;
+    const int head = min(nb, (int)((16u - (uint32_t)((uintptr_t)to & 15u)) & 15u));
+    auto byte_at = [&](int i) { return stage[(int)list[i / p.R] * p.R + i % p.R]; };
+    for (int i = tid; i < head; i += kCopyNT) to[i] = byte_at(i);
+    const int np = (nb - head) / 16;
+    for (int i = tid; i < np; i += kCopyNT) {
+      const int at = head + 16 * i;
+      int r = at / p.R, x = at - r * p.R;  // x is a multiple of U, as the destination's offset and R are
+      uint32_t w[4];
+      const uint8_t *row = stage + (int)list[r] * p.R;
+#pragma unroll
+      for (int e = 0; e < 16 / U; ++e) {
+        if constexpr (U == 8) {
+          const uint2 q = *reinterpret_cast<const uint2 *>(row + x);
+          w[2 * e] = q.x;
+          w[2 * e + 1] = q.y;
+        } else if constexpr (U == 4) {
+          w[e] = *reinterpret_cast<const uint32_t *>(row + x);
+        } else if constexpr (U == 2) {
+          const uint32_t q = *reinterpret_cast<const uint16_t *>(row + x);
+          w[e / 2] = (e % 2) ? (w[e / 2] | (q << 16)) : q;
+        } else {
+          const uint32_t q = row[x];
+          w[e / 4] = (e % 4) ? (w[e / 4] | (q << (8 * (e % 4)))) : q;
+        }
+        x += U;
+        if (x == p.R && e + 1 < 16 / U) {
+          x = 0;
+          row = stage + (int)list[++r] * p.R;
+        }
+      }
+      *reinterpret_cast<uint4 *>(to + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for (int i = head + 16 * np + tid; i < nb; i += kCopyNT) to[i] = byte_at(i);
+  }
+  float *ao = p.acc_out + b * p.acc_ostride;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (tid + k * kCopyNT < n) ao[dst + tid + k * kCopyNT] = av[k];
+  // in place, the freed positions start from zero weight; they are this chunk's own
+  if (p.in_place)
+    for (int t = tid; t < rows_here; t += kCopyNT)
+      if (t0 + t >= after) ao[t0 + t] = 0.f;
+}
+
+template <int U>
+cudaError_t launch_copy(const CopyParams &p, cudaStream_t st) {
+  const size_t smem = U < 16 ? align_up((size_t)p.chunk * p.R, 16) : 0;
+  cudaError_t e = ensure_smem_limit((const void *)evict_compact<U>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_compact<U>, dim3((unsigned)(p.B * p.nchunk)), dim3(kCopyNT), smem, st, p);
+}
+
+}  // namespace evict
+
+size_t evict_workspace_bytes(int64_t B, int64_t T, int R) { return evict::plan_of(B, T, R).total; }
+int64_t evict_jobs(int64_t B, int64_t T, int R) { return B * evict::plan_of(B, T, R).nchunk; }
+
+cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc, int64_t acc_stride,
+                         const int32_t *lens, int64_t B, int64_t T, int64_t n_keep, int64_t n_recent, int R,
+                         uint8_t *out, int64_t ostride, float *acc_out, int64_t acc_ostride, int32_t *lens_out,
+                         int32_t *kept, uint8_t *ws, cudaStream_t st) {
+  using namespace evict;
+  const Plan pl = plan_of(B, T, R);
+  SelectParams sp{acc, acc_stride, lens, T, n_keep, n_recent, (int32_t *)(ws + pl.off_rows),
+                  (uint32_t *)(ws + pl.off_bits), (int32_t *)(ws + pl.off_off), (uint32_t *)(ws + pl.off_flag),
+                  (uint32_t *)(ws + pl.off_ticket), (uint32_t *)ws, lens_out, kept, pl.nchunk, pl.words, pl.chunk};
+  // one CTA of the cluster per four steps of tokens
+  int cs = 1;
+  while (cs < kMaxCluster && T > (int64_t)cs * 4 * kPieceTok) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(B * cs));
+  cfg.blockDim = dim3(kNT);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, sp);
+  if (e != cudaSuccess) return e;
+  CopyParams cp{codes, out, bstride, ostride, acc, acc_out, acc_stride, acc_ostride, kept, sp.rows, sp.bits, sp.off,
+                sp.flag, sp.ticket, (uint32_t *)ws, B, n_keep, pl.nchunk, pl.words, R, pl.chunk, out == codes};
+  if (R % 16 == 0 && pl.chunk * R <= kCopyBytes) return launch_copy<16>(cp, st);
+  if (R % 8 == 0) return launch_copy<8>(cp, st);
+  if (R % 4 == 0) return launch_copy<4>(cp, st);
+  if (R % 2 == 0) return launch_copy<2>(cp, st);
+  return launch_copy<1>(cp, st);
+}
+
+}  // namespace fsq

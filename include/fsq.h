@@ -279,6 +279,66 @@ FSQ_API fsq_status fsq_decode_attn_multi(const uint16_t *q, int64_t B, int n_new
 FSQ_API const char *fsq_decode_attn_kernel(int64_t B, int n_new, int64_t T, int n_q, int n_kv, int d_h, int G,
                                            const fsq_attn_opts *opts);
 
+/* Head norms with rotary positions: queries, and keys that a caller forms
+ * itself, as the attention calls with rope_knorm expect them (the same map they
+ * apply to the keys they rebuild, [S] eq. 5), in one pass:
+ *   y = x / sqrt(mean_d x_d^2 + eps) * gain      per token and head
+ *   (y_i, y_{i+64}) rotated by p * rope_base^(-2i/128), i = 0..63
+ *  q, k      bf16 [n_tok, heads, d_h]: token t at q + t*ldq, its heads d_h apart
+ *            (so the heads of a fused projection are read in place)   — read
+ *  q_gain, k_gain  device bf16 [d_h], NULL = ones
+ *  q_out, k_out    bf16, token strides ldq_out, ldk_out             — written;
+ *            each may be its own input with the same stride (in place), and
+ *            otherwise overlaps no input and no other output
+ *  positions device int32 [n_tok], NULL = 0, 1, 2, ..: token t is at position
+ *            pos0 + positions[t] (a decode step passes seq_lens and pos0 = -1)
+ * The sum of squares, the norm and the rotation are fp32; the angle is reduced
+ * in 64 bits, so far positions keep their precision; one rounding to bf16.
+ * n_k == 0: queries only (k, k_gain and k_out are not looked at).  n_tok == 0 is
+ * a no-op.  Needs: d_h == 128, n_q >= 1, n_k >= 0, n_q + n_k <= 65535; strides
+ * of at least heads*d_h (unless n_tok == 1), multiples of 8; pointers 16-byte
+ * aligned (positions 4-byte); eps >= 0, rope_base > 1, n_tok <= 2^31 - 1. */
+FSQ_API fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,
+                                    int64_t ldq_out, const uint16_t *k, int64_t ldk, int n_k, const uint16_t *k_gain,
+                                    uint16_t *k_out, int64_t ldk_out, int64_t n_tok, int d_h,
+                                    const int32_t *positions, int64_t pos0, float eps, float rope_base,
+                                    fsq_stream_t stream);
+
+/* Eviction by accumulated attention weight.  Row b holds L_b tokens (T, or
+ * seq_lens[b]) and a weight acc[b][t] for each.  A row of more than n_keep
+ * tokens keeps its last n_recent and, of the others, the n_keep - n_recent of
+ * the largest weight (equal weights: the lowest index first; NaN counts as
+ * below every number); a shorter row keeps everything.  Kept tokens stay in
+ * order at the front of the row; the cache index of a token is its position from
+ * then on (with rope_knorm, later attention rotates keys by it).
+ *  codes      uint8 cache [B][T.. rows of R bytes], batch stride in bytes  — read
+ *  acc        fp32 [B][T..], acc_stride elements between rows              — read
+ *  seq_lens   device int32 [B], 0 <= seq_lens[b] <= T, or NULL; a value outside
+ *             is clamped and records FSQ_ERR_INVALID_ARG in the error word
+ *  codes_out, acc_out, out_stride_bytes, acc_out_stride: where the kept rows
+ *             and weights go, [B][n_keep..]                            — written
+ *  In place: codes_out == codes and acc_out == acc with equal strides; then the
+ *  weights of the freed positions are set to 0, so that tokens appended there
+ *  start from 0.  Otherwise nothing of the outputs may overlap the inputs, and
+ *  only the kept tokens' rows and weights are written.
+ *  lens_out   device int32 [B], the new lengths min(L_b, n_keep), or NULL; may be
+ *             seq_lens                                                 — written
+ *  kept       device int32 [B, n_keep], the kept tokens' old indices, ascending,
+ *             -1 behind the last, or NULL                              — written
+ *  workspace  >= fsq_cache_evict_workspace_size(...) bytes, 256-byte aligned; its
+ *             error word is read with fsq_workspace_status
+ * Needs: L in {4, 16, 256} (0 = 16) and the G rules of the append; 0 <= T <=
+ * 2^31 - 1; 1 <= n_keep, 0 <= n_recent <= n_keep <= 2^31 - 1; strides that
+ * hold their rows; codes, codes_out and their strides 16-byte aligned, acc,
+ * seq_lens and the other outputs 4-byte aligned; B * T / 32 <= 2^31 - 1.
+ * B == 0 and T == 0 are no-ops (T == 0 leaves lens_out and kept as they were). */
+FSQ_API size_t fsq_cache_evict_workspace_size(int64_t B, int64_t T, int G, int levels);
+FSQ_API fsq_status fsq_cache_evict(const uint8_t *codes, int64_t code_batch_stride_bytes, const float *acc,
+                                   int64_t acc_stride, const int32_t *seq_lens, int64_t B, int64_t T, int64_t n_keep,
+                                   int64_t n_recent, int G, int levels, uint8_t *codes_out, int64_t out_stride_bytes,
+                                   float *acc_out, int64_t acc_out_stride, int32_t *lens_out, int32_t *kept,
+                                   void *workspace, size_t workspace_bytes, fsq_stream_t stream);
+
 /* Allocation-free decode attention.  There is no counterpart in the paper:
  * this entry point exists for callers that cannot allocate device memory at
  * the point where they decode — for example a plugin whose host framework

@@ -350,6 +350,59 @@ def partial_attn(s, V):
 
 
 # ---------------------------------------------------------------------------
+# Serving operators around the cache
+# ---------------------------------------------------------------------------
+def norm_rope(x, gain, positions, eps, base):
+    """N_k then RoPE_t of [n_tok, heads, d] at the given positions, every head
+    alike (the map of reconstruct_kv's keys, for queries and keys a caller forms)."""
+    x = np.asarray(x, dtype=np.float64)
+    y = rms_norm(x, np.ones(x.shape[-1]) if gain is None else gain, eps)
+    return np.stack([rope(y[:, h], positions, base) for h in range(x.shape[1])], axis=1)
+
+
+def decode_attn_prefix(q, prefix, codes, W_kv, n_kv, G, scale=None, lengths=None, levels=LEVELS):
+    """Decode attention whose rows share the cached tokens `prefix` [T_p, R] and
+    continue with their own codes[b] ([T, R], the first lengths[b] of them): the
+    attention of each row over the concatenation."""
+    q = np.asarray(q, dtype=np.float64)
+    o = np.empty(q.shape)
+    for b in range(q.shape[0]):
+        n = codes.shape[1] if lengths is None else int(lengths[b])
+        row = np.concatenate([prefix, codes[b, :n]])
+        o[b] = decode_attn(q[b:b + 1], row[None], W_kv, n_kv, G, scale=scale, levels=levels)[0]
+    return o
+
+
+def attn_weights(q, codes, W_kv, n_kv, G, scale=None, lengths=None, levels=LEVELS):
+    """Attention weight of every cached token, summed over the query heads:
+    [B, T], 0 behind a row's length."""
+    q = np.asarray(q, dtype=np.float64)
+    B, n_q, d_h = q.shape
+    scale = 1.0 / math.sqrt(d_h) if scale is None else scale
+    Wk, _ = split_wkv(W_kv, n_kv, d_h)
+    w = np.zeros((B, codes.shape[1]))
+    for b in range(B):
+        n = codes.shape[1] if lengths is None else int(lengths[b])
+        z = unpack(codes[b, :n], G, levels).astype(np.float64)
+        for h in range(n_q):
+            w[b, :n] += softmax(scale * ((z @ Wk[h // (n_q // n_kv)].T) @ q[b, h]))
+    return w
+
+
+def evict(acc, length, n_keep, n_recent):
+    """Indices (ascending) of the tokens a row of `length` tokens keeps: the last
+    n_recent and the heaviest of the others, n_keep in all; equal weights go to
+    the lowest index, NaN is below every number.  Plain selection, one at a time
+    in order of weight."""
+    if length <= n_keep:
+        return np.arange(length)
+    a = np.asarray(acc, dtype=np.float64)[: length - n_recent]
+    key = [(0, 0.0, i) if math.isnan(v) else (-1, -v, i) for i, v in enumerate(a)]
+    best = [k[2] for k in sorted(key)][: n_keep - n_recent]
+    return np.array(sorted(best) + list(range(length - n_recent, length)), dtype=np.int64)
+
+
+# ---------------------------------------------------------------------------
 # Byte budgeting ([S] Byte Budgeting; [D] kernel frame)
 # ---------------------------------------------------------------------------
 def code_bytes_per_token(G, bits=BITS):

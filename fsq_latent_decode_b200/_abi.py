@@ -31,7 +31,8 @@ EXPORTED = ("fsq_attn_opts_default", "fsq_thresholds", "fsq_encode_pack", "fsq_q
             "fsq_decode_attn_workspace_size", "fsq_decode_attn", "fsq_workspace_status",
             "fsq_status_string", "fsq_format_version", "fsq_decode_attn_noalloc",
             "fsq_decode_attn_noalloc_status", "fsq_decode_attn_multi_workspace_size", "fsq_decode_attn_multi",
-            "fsq_decode_attn_kernel", "fsq_qk_norm_rope", "fsq_cache_evict_workspace_size", "fsq_cache_evict")
+            "fsq_decode_attn_kernel", "fsq_qk_norm_rope", "fsq_cache_evict_workspace_size", "fsq_cache_evict",
+            "fsq_decode_attn_prefix_workspace_size", "fsq_decode_attn_prefix")
 # FSQ_NOALLOC_SCRATCH_BYTES of include/fsq.h (a host test checks the two agree)
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -89,6 +90,11 @@ def _load() -> C.CDLL:
     lib.fsq_decode_attn_noalloc.restype = i32
     lib.fsq_decode_attn_noalloc_status.argtypes = [vp]
     lib.fsq_decode_attn_noalloc_status.restype = i32
+    lib.fsq_decode_attn_prefix_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i32, C.POINTER(AttnOpts)]
+    lib.fsq_decode_attn_prefix_workspace_size.restype = C.c_size_t
+    lib.fsq_decode_attn_prefix.argtypes = [vp, i64, i32, i32, vp, i64, vp, i64, i64, i32, vp, i32,
+                                           C.POINTER(AttnOpts), vp, C.c_size_t, vp, vp]
+    lib.fsq_decode_attn_prefix.restype = i32
     lib.fsq_qk_norm_rope.argtypes = [vp, i64, i32, vp, vp, i64, vp, i64, i32, vp, vp, i64, i64, i32, vp, i64, f32,
                                      f32, vp]
     lib.fsq_qk_norm_rope.restype = i32
@@ -247,6 +253,18 @@ def decode_attn_noalloc_raw(q_ptr, B, n_q, d_h, codes_ptr, bstride, T, G, wkv_pt
 def decode_attn_noalloc_status(stream=None) -> int:
     """Device status of the last allocation-free decode call on this device (blocking)."""
     return _lib().fsq_decode_attn_noalloc_status(_stream_ptr(stream))
+
+
+def prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts: AttnOpts | None = None) -> int:
+    return int(_lib().fsq_decode_attn_prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G,
+                                                            None if opts is None else C.byref(opts)))
+
+
+def decode_attn_prefix_raw(q_ptr, B, n_q, d_h, prefix_ptr, T_prefix, codes_ptr, bstride, T, G, wkv_ptr, n_kv, opts,
+                           ws_ptr, ws_bytes, o_ptr, stream_ptr) -> int:
+    return _lib().fsq_decode_attn_prefix(q_ptr, B, n_q, d_h, prefix_ptr, T_prefix, codes_ptr, bstride, T, G, wkv_ptr,
+                                         n_kv, None if opts is None else C.byref(opts), ws_ptr, ws_bytes, o_ptr,
+                                         stream_ptr)
 
 
 def qk_norm_rope_raw(*args) -> int:
@@ -451,6 +469,48 @@ def _cache_stride(codes, rb, T, what):
         raise ValueError(f"{what} must be [B, T_max >= {T}, {rb}] uint8 with contiguous rows")
     # a size-1 leading dim may carry any stride
     return codes.stride(0) if codes.shape[0] > 1 else (codes.shape[1] * rb + 15) // 16 * 16
+
+
+def _attn_inputs(q, W_kv, n_kv, G, opts):
+    """Checks q [B, n_q, 128] and W_kv [2 n_kv 128, G], contiguous bf16; returns opts and the row bytes."""
+    import torch
+    _of_type(q, torch.bfloat16, "q")
+    _of_type(W_kv, torch.bfloat16, "W_kv")
+    if q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be contiguous [B, n_q, d_h]")
+    if tuple(W_kv.shape) != (2 * n_kv * q.shape[2], G) or not W_kv.is_contiguous():
+        raise ValueError("W_kv must be contiguous [2 * n_kv * d_h, G]")
+    if opts is None:
+        opts = attn_opts()
+    return opts, row_bytes(G, opts.levels or 16)
+
+
+def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, workspace=None, out=None, stream=None):
+    """o[B, n_q, 128] of rows that share the cached tokens prefix[:T_prefix]
+    (uint8 [T.., R]) and continue with their own codes[b, :T] (opts.seq_lens[b]
+    of them, 0 included; codes may be None when T is 0).  Absorbed form."""
+    import torch
+    opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
+    B, n_q, d_h = q.shape
+    _of_type(prefix, torch.uint8, "prefix")
+    _of_type(codes, torch.uint8, "codes")
+    if prefix.dim() != 2 or prefix.shape[0] < T_prefix or prefix.shape[1] != rb or not prefix.is_contiguous():
+        raise ValueError(f"prefix must be contiguous [at least {T_prefix}, {rb}]")
+    if T > 0 and (codes is None or codes.shape[0] != B):
+        raise ValueError("codes must hold the own tokens of every row")
+    stride = _cache_stride(codes, rb, T, "codes") if T > 0 else 0
+    dtype = torch.float32 if opts.out_fp32 else torch.bfloat16
+    if out is not None and (out.shape != q.shape or out.dtype != dtype or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
+    _on_current_device("decode_attn_prefix", q, prefix, codes, W_kv, out, *opts._tensors)
+    if out is None:
+        out = torch.empty((B, n_q, d_h), dtype=dtype, device=q.device)
+    nbytes = prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts)
+    ws = (workspace or Workspace(q.device)).get(nbytes)
+    st = decode_attn_prefix_raw(_ptr(q), B, n_q, d_h, _ptr(prefix), T_prefix, _opt_ptr(codes), stride, T, G, _ptr(W_kv),
+                                n_kv, opts, _ptr(ws), ws.numel(), _ptr(out), _stream_ptr(stream))
+    _check(st, "fsq_decode_attn_prefix")
+    return out
 
 
 def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=None, out=None, acc_out=None,

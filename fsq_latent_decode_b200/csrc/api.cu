@@ -50,6 +50,15 @@ cudaError_t launch_absorbed_tc(const uint16_t *q, const uint8_t *codes, int64_t 
                                const uint16_t *W_kv, float scale, int S, int64_t tps, uint8_t *qphys, float *corr,
                                float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32,
                                uint32_t stall_ns, void *const *prof, cudaStream_t st);
+bool prefix_supported(int n_q, int G);
+int prefix_rows_per_tile(int n_q);
+int prefix_tile_tokens();
+size_t prefix_query_bytes(int G);
+cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, int d_h, const uint8_t *shared, int64_t Tp,
+                          const uint8_t *codes, int64_t bstride, int64_t T, const int32_t *seq_lens, int G, int bits,
+                          const uint16_t *W_kv, float scale, int QT, int Sp, int Ss, int k, uint8_t *qbuf, float *sig,
+                          float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32, uint32_t stall_ns,
+                          void *const *prof, cudaStream_t st);
 cudaError_t launch_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,
                              int64_t ldqo, const uint16_t *k, int64_t ldk, int n_k, const uint16_t *k_gain,
                              uint16_t *k_out, int64_t ldko, int64_t n_tok, const int32_t *positions, int64_t pos0,
@@ -210,6 +219,68 @@ fsq_status plan_decode(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G, 
   p->off_part = off;
   off = align_up(off + sizeof(float) * (size_t)Bc * S * n_q * (2 + acc_len), 256);
   if (variant == FSQ_VARIANT_ABSORBED || variant == FSQ_VARIANT_HYBRID) p->mp = merge_plan((int)S, Bc, n_q, n_kv, acc_len);
+  p->off_mslab = off;
+  off = align_up(off + p->mp.slab_bytes, 256);
+  p->off_mcnt = off;
+  off = align_up(off + p->mp.cnt_bytes, 256);
+  p->total = off;
+  return FSQ_OK;
+}
+
+// Shared-prefix attention: query tiles, splits, workspace.
+struct PrefixPlan {
+  int levels, QT, Sp, Ss, k;  // k: tiles of a split, of the prefix and of a row's own tokens alike
+  MergePlan mp;
+  size_t off_q, off_sig, off_part, off_mslab, off_mcnt, total;
+};
+
+fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int d_h, int G, const fsq_attn_opts &op,
+                       PrefixPlan *p) {
+  if (B < 0 || Tp < 1 || T < 0 || n_q < 1 || n_kv < 1 || d_h < 1 || G < 2) return FSQ_ERR_INVALID_ARG;
+  if (n_q % n_kv) return FSQ_ERR_INVALID_ARG;
+  if (op.variant < FSQ_VARIANT_AUTO || op.variant > FSQ_VARIANT_HYBRID || op.num_splits < 0) return FSQ_ERR_INVALID_ARG;
+  if (op.rope_knorm != 0 && op.rope_knorm != 1) return FSQ_ERR_INVALID_ARG;
+  const int L = levels_of(op.levels);
+  if (!L || !width_ok(G, L) || d_h != FSQ_HEAD_DIM || !prefix_supported(n_q, G)) return FSQ_ERR_UNSUPPORTED;
+  if (op.rope_knorm || op.variant > FSQ_VARIANT_ABSORBED || B > kMaxGridRows) return FSQ_ERR_UNSUPPORTED;
+  const int64_t tile = prefix_tile_tokens(), Bc = B > 0 ? B : 1;
+  const int64_t nt = (Tp + tile - 1) / tile, no = (T + tile - 1) / tile, most = nt > no ? nt : no;
+  if (most > INT32_MAX / 2) return FSQ_ERR_UNSUPPORTED;
+  const int64_t rpt = prefix_rows_per_tile(n_q), QT = (Bc + rpt - 1) / rpt;
+  // Tiles per split.  Every CTA costs its tiles and a fixed start and end, runs
+  // of CTAs beyond one per SM follow one another, and every split of a row
+  // leaves a partial that is written and merged: the cheapest k by these rates
+  // (measured at G = 256, n_q = 32: 0.6 us a tile, 5 us a CTA, partials at 3 TB/s).
+  int64_t k = 0;
+  if (op.num_splits > 0) {
+    const int64_t s = op.num_splits < nt ? op.num_splits : nt;
+    k = (nt + s - 1) / s;
+  } else {
+    double best = 0;
+    for (int s = 1; s <= kNumSMs; ++s) {
+      const int64_t kk = (most + s - 1) / s;
+      const int64_t sp = (nt + kk - 1) / kk, so = (no + kk - 1) / kk, ctas = QT * sp + Bc * so;
+      const double cost = (double)((ctas + kNumSMs - 1) / kNumSMs) * (0.6 * kk + 5.0) +
+                          8e-6 / 3.0 * (double)(sp + so) * Bc * n_q * (G + 2);
+      if (s == 1 || cost < best) best = cost, k = kk;
+      if (kk == 1) break;
+    }
+  }
+  const int64_t Sp = (nt + k - 1) / k, Ss = (no + k - 1) / k;
+  if (QT * Sp + Bc * Ss > INT32_MAX) return FSQ_ERR_UNSUPPORTED;
+  p->levels = L;
+  p->QT = (int)QT;
+  p->Sp = (int)Sp;
+  p->Ss = (int)Ss;
+  p->k = (int)k;
+  size_t off = kWsHeader;
+  p->off_q = off;
+  off = align_up(off + prefix_query_bytes(G) * (size_t)Bc * n_q, 256);
+  p->off_sig = off;
+  off = align_up(off + sizeof(float) * (size_t)Bc * n_q, 256);
+  p->off_part = off;
+  off = align_up(off + sizeof(float) * (size_t)Bc * (Sp + Ss) * n_q * (2 + G), 256);
+  p->mp = merge_plan((int)(Sp + Ss), Bc, n_q, n_kv, G);
   p->off_mslab = off;
   off = align_up(off + p->mp.slab_bytes, 256);
   p->off_mcnt = off;
@@ -386,6 +457,45 @@ fsq_status fsq_decode_attn_multi(const uint16_t *q, int64_t B, int n_new, int n_
                            err, o, op.out_fp32, op.prof_events, s);
   }
   return from_cuda(e);
+}
+
+size_t fsq_decode_attn_prefix_workspace_size(int64_t B, int64_t T_prefix, int64_t T, int n_q, int n_kv, int d_h, int G,
+                                             const fsq_attn_opts *opts) {
+  fsq_attn_opts op;
+  if (opts) op = *opts;
+  else fsq_attn_opts_default(&op);
+  PrefixPlan p;
+  return plan_prefix(B, T_prefix, T, n_q, n_kv, d_h, G, op, &p) == FSQ_OK ? p.total : 0;
+}
+
+fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q, int d_h, const uint8_t *prefix_codes,
+                                  int64_t T_prefix, const uint8_t *codes, int64_t code_batch_stride_bytes, int64_t T,
+                                  int G, const uint16_t *W_kv, int n_kv, const fsq_attn_opts *opts, void *workspace,
+                                  size_t workspace_bytes, void *o, fsq_stream_t stream) {
+  fsq_attn_opts op;
+  if (opts) op = *opts;
+  else fsq_attn_opts_default(&op);
+  PrefixPlan p;
+  const fsq_status st = plan_prefix(B, T_prefix, T, n_q, n_kv, d_h, G, op, &p);
+  if (st != FSQ_OK) return st;
+  if (B == 0) return FSQ_OK;
+  if (!q || !prefix_codes || !W_kv || !o || (T > 0 && !codes)) return FSQ_ERR_INVALID_ARG;
+  const int bits = bits_of_levels(p.levels);
+  if (T > 0 && code_batch_stride_bytes < T * ((int64_t)G * bits / 8)) return FSQ_ERR_INVALID_ARG;
+  if (!aligned16(prefix_codes) || (T > 0 && (!aligned16(codes) || code_batch_stride_bytes % 16)))
+    return FSQ_ERR_MISALIGNED;
+  if (!aligned16(q) || !aligned16(W_kv) || !aligned16(o)) return FSQ_ERR_MISALIGNED;
+  if ((uintptr_t)op.seq_lens & 3u) return FSQ_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < p.total) return FSQ_ERR_WORKSPACE;
+  if ((uintptr_t)workspace & 255u) return FSQ_ERR_MISALIGNED;
+  char *ws = (char *)workspace;
+  MergeScratch ms{nullptr, nullptr, 0};
+  if (p.mp.cnt_bytes) ms = {(float *)(ws + p.off_mslab), (uint32_t *)(ws + p.off_mcnt), (int)(B * n_kv)};
+  return from_cuda(launch_prefix(q, B, n_q, n_kv, d_h, prefix_codes, T_prefix, codes, code_batch_stride_bytes, T,
+                                 op.seq_lens, G, bits, W_kv, op.scale > 0.f ? op.scale : 1.f / sqrtf((float)d_h), p.QT,
+                                 p.Sp, p.Ss, p.k, (uint8_t *)(ws + p.off_q), (float *)(ws + p.off_sig),
+                                 (float *)(ws + p.off_part), (uint32_t *)ws, ms, o, op.out_fp32, op.debug_stall_ns,
+                                 op.prof_events, (cudaStream_t)stream));
 }
 
 fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,

@@ -279,6 +279,31 @@ FSQ_API fsq_status fsq_decode_attn_multi(const uint16_t *q, int64_t B, int n_new
 FSQ_API const char *fsq_decode_attn_kernel(int64_t B, int n_new, int64_t T, int n_q, int n_kv, int d_h, int G,
                                            const fsq_attn_opts *opts);
 
+/* Single-token attention of a batch whose rows share a long prefix (a system
+ * prompt, a document asked many questions): the prefix's codes are stored once
+ * and each of its tiles is read, dequantised and multiplied once for all rows.
+ * Row b attends to the T_prefix shared tokens and then to its own tokens
+ * codes[b][0 .. T-1] (0 .. seq_lens[b]-1 with opts->seq_lens; there T is the
+ * longest row, and 0 <= seq_lens[b] <= T; a value outside is clamped and
+ * records FSQ_ERR_INVALID_ARG in the error word).  The result is that of
+ * fsq_decode_attn on the concatenated rows.
+ *  prefix_codes  uint8 [T_prefix] rows of R bytes, 16-byte aligned        — read
+ *  codes         as in fsq_decode_attn; not looked at when T == 0         — read
+ *  q, W_kv, o, opts, workspace (fsq_decode_attn_prefix_workspace_size): as in
+ *  fsq_decode_attn, except that q is read after the kernels before it; the
+ *  form is the absorbed one (variant AUTO or ABSORBED, rope_knorm 0; others
+ *  return FSQ_ERR_UNSUPPORTED).  opts->num_splits counts splits of the prefix.
+ * Q' = W_k^T q is held in fp16, scaled per head (11 significant bits).
+ * Needs: d_h == 128, n_q % n_kv == 0, n_q <= 128, G <= 256 and the G rules of
+ * the append, T_prefix >= 1, T >= 0, B <= 65535.  B == 0 is a no-op. */
+FSQ_API size_t fsq_decode_attn_prefix_workspace_size(int64_t B, int64_t T_prefix, int64_t T, int n_q, int n_kv,
+                                                     int d_h, int G, const fsq_attn_opts *opts);
+FSQ_API fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q, int d_h,
+                                          const uint8_t *prefix_codes, int64_t T_prefix, const uint8_t *codes,
+                                          int64_t code_batch_stride_bytes, int64_t T, int G, const uint16_t *W_kv,
+                                          int n_kv, const fsq_attn_opts *opts, void *workspace,
+                                          size_t workspace_bytes, void *o, fsq_stream_t stream);
+
 /* Head norms with rotary positions: queries, and keys that a caller forms
  * itself, as the attention calls with rope_knorm expect them (the same map they
  * apply to the keys they rebuild, [S] eq. 5), in one pass:

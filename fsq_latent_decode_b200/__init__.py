@@ -14,7 +14,8 @@ from ._abi import (  # noqa: F401
     multi_workspace_size, split_kernel, encode_opts, encode_pack, encode_pack_raw, quant_params,
     quantize_pack_f32, quantize_pack_f32_raw, row_bytes, bits_of_levels, status_string, thresholds, workspace_size,
     workspace_status, qk_norm_rope, qk_norm_rope_raw, cache_evict, cache_evict_raw, cache_evict_workspace_size,
-    decode_attn_prefix, decode_attn_prefix_raw, prefix_workspace_size,
+    decode_attn_prefix, decode_attn_prefix_raw, prefix_workspace_size, attn_weights, attn_weights_raw,
+    attn_weights_workspace_size,
 )
 
 
@@ -25,4 +26,4 @@ def __getattr__(name):  # `lib` (the loaded libfsq.so) is mapped on first access
     raise AttributeError(name)
 
 __all__ = ["encode_pack", "quantize_pack_f32", "decode_attn", "decode_attn_multi", "attn_opts", "thresholds", "workspace_size",
-           "Workspace", "FsqError", "qk_norm_rope", "cache_evict", "decode_attn_prefix"]
+           "Workspace", "FsqError", "qk_norm_rope", "cache_evict", "decode_attn_prefix", "attn_weights"]

@@ -32,7 +32,8 @@ EXPORTED = ("fsq_attn_opts_default", "fsq_thresholds", "fsq_encode_pack", "fsq_q
             "fsq_status_string", "fsq_format_version", "fsq_decode_attn_noalloc",
             "fsq_decode_attn_noalloc_status", "fsq_decode_attn_multi_workspace_size", "fsq_decode_attn_multi",
             "fsq_decode_attn_kernel", "fsq_qk_norm_rope", "fsq_cache_evict_workspace_size", "fsq_cache_evict",
-            "fsq_decode_attn_prefix_workspace_size", "fsq_decode_attn_prefix")
+            "fsq_decode_attn_prefix_workspace_size", "fsq_decode_attn_prefix",
+            "fsq_attn_weights_workspace_size", "fsq_attn_weights")
 # FSQ_NOALLOC_SCRATCH_BYTES of include/fsq.h (a host test checks the two agree)
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -95,6 +96,11 @@ def _load() -> C.CDLL:
     lib.fsq_decode_attn_prefix.argtypes = [vp, i64, i32, i32, vp, i64, vp, i64, i64, i32, vp, i32,
                                            C.POINTER(AttnOpts), vp, C.c_size_t, vp, vp]
     lib.fsq_decode_attn_prefix.restype = i32
+    lib.fsq_attn_weights_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32, C.POINTER(AttnOpts)]
+    lib.fsq_attn_weights_workspace_size.restype = C.c_size_t
+    lib.fsq_attn_weights.argtypes = [vp, i64, i32, i32, vp, i64, i64, i32, vp, i32, C.POINTER(AttnOpts), vp, i64, vp,
+                                     C.c_size_t, vp]
+    lib.fsq_attn_weights.restype = i32
     lib.fsq_qk_norm_rope.argtypes = [vp, i64, i32, vp, vp, i64, vp, i64, i32, vp, vp, i64, i64, i32, vp, i64, f32,
                                      f32, vp]
     lib.fsq_qk_norm_rope.restype = i32
@@ -265,6 +271,18 @@ def decode_attn_prefix_raw(q_ptr, B, n_q, d_h, prefix_ptr, T_prefix, codes_ptr, 
     return _lib().fsq_decode_attn_prefix(q_ptr, B, n_q, d_h, prefix_ptr, T_prefix, codes_ptr, bstride, T, G, wkv_ptr,
                                          n_kv, None if opts is None else C.byref(opts), ws_ptr, ws_bytes, o_ptr,
                                          stream_ptr)
+
+
+def attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts: AttnOpts | None = None) -> int:
+    return int(_lib().fsq_attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G,
+                                                      None if opts is None else C.byref(opts)))
+
+
+def attn_weights_raw(q_ptr, B, n_q, d_h, codes_ptr, bstride, T, G, wkv_ptr, n_kv, opts, acc_ptr, acc_stride, ws_ptr,
+                     ws_bytes, stream_ptr) -> int:
+    return _lib().fsq_attn_weights(q_ptr, B, n_q, d_h, codes_ptr, bstride, T, G, wkv_ptr, n_kv,
+                                   None if opts is None else C.byref(opts), acc_ptr, acc_stride, ws_ptr, ws_bytes,
+                                   stream_ptr)
 
 
 def qk_norm_rope_raw(*args) -> int:
@@ -513,6 +531,34 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
     return out
 
 
+def _acc_stride(t, B, n, what):
+    """Row stride of a [B, at least n] tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [B, at least {n}] with contiguous rows")
+    return t.stride(0) if B > 1 else max(t.stride(0), t.shape[1])
+
+
+def attn_weights(q, codes, W_kv, acc, T, n_kv, G, opts=None, workspace=None, stream=None):
+    """Adds to acc[b, t] (fp32 [B, at least T]) the attention weight of token t of
+    codes[b, :T] for the queries q [B, n_q, 128], summed over the heads; with
+    opts.seq_lens row b holds that many tokens.  Returns acc."""
+    import torch
+    opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
+    B, n_q, d_h = q.shape
+    _of_type(codes, torch.uint8, "codes")
+    _of_type(acc, torch.float32, "acc")
+    if codes.shape[0] != B:
+        raise ValueError("codes must hold a row for every query")
+    cs, as_ = _cache_stride(codes, rb, T, "codes"), _acc_stride(acc, B, T, "acc")
+    _on_current_device("attn_weights", q, codes, W_kv, acc, *opts._tensors)
+    nbytes = attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts)
+    ws = (workspace or Workspace(q.device)).get(nbytes)
+    st = attn_weights_raw(_ptr(q), B, n_q, d_h, _ptr(codes), cs, T, G, _ptr(W_kv), n_kv, opts, _ptr(acc), as_, _ptr(ws),
+                          ws.numel(), _stream_ptr(stream))
+    _check(st, "fsq_attn_weights")
+    return acc
+
+
 def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=None, out=None, acc_out=None,
                 lens_out=None, kept=None, workspace=None, stream=None):
     """Keeps each row's last n_recent tokens and the heaviest of the others,
@@ -533,11 +579,7 @@ def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=No
     _of_type(out, torch.uint8, "out")
     _of_type(acc_out, torch.float32, "acc_out")
     n_out = T if out is codes else min(T, n_keep)
-    strides = []
-    for t, n, what in ((acc, T, "acc"), (acc_out, n_out, "acc_out")):
-        if t.dim() != 2 or t.shape[0] != B or t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what} must be [B, at least {n}] with contiguous rows")
-        strides.append(t.stride(0) if B > 1 else max(t.stride(0), t.shape[1]))
+    as_, aos = _acc_stride(acc, B, T, "acc"), _acc_stride(acc_out, B, n_out, "acc_out")
     if out.shape[0] != B:
         raise ValueError("out must hold the rows of codes")
     for t, shape, what in ((seq_lens, (B,), "seq_lens"), (lens_out, (B,), "lens_out"), (kept, (B, n_keep), "kept")):
@@ -550,8 +592,8 @@ def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=No
     cs, os_ = _cache_stride(codes, rb, T, "codes"), _cache_stride(out, rb, n_out, "out")
     _on_current_device("cache_evict", codes, acc, out, acc_out, seq_lens, lens_out, kept)
     ws = (workspace or Workspace(codes.device)).get(nbytes)
-    st = cache_evict_raw(_ptr(codes), cs, _ptr(acc), strides[0], _opt_ptr(seq_lens), B, T, n_keep, n_recent, G, levels,
-                         _ptr(out), os_, _ptr(acc_out), strides[1], _opt_ptr(lens_out), _opt_ptr(kept), _ptr(ws),
+    st = cache_evict_raw(_ptr(codes), cs, _ptr(acc), as_, _opt_ptr(seq_lens), B, T, n_keep, n_recent, G, levels,
+                         _ptr(out), os_, _ptr(acc_out), aos, _opt_ptr(lens_out), _opt_ptr(kept), _ptr(ws),
                          ws.numel(), _stream_ptr(stream))
     _check(st, "fsq_cache_evict")
     return out, acc_out

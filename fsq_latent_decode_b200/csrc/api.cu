@@ -59,6 +59,13 @@ cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, int d
                           const uint16_t *W_kv, float scale, int QT, int Sp, int Ss, int k, uint8_t *qbuf, float *sig,
                           float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32, uint32_t stall_ns,
                           void *const *prof, cudaStream_t st);
+bool weights_supported(int n_q, int G, int bits);
+int weights_tile_tokens();
+size_t weights_query_bytes(int n_q, int G, int bits);
+cudaError_t launch_weights(const uint16_t *q, int64_t B, int n_q, int n_kv, const uint8_t *codes, int64_t bstride,
+                           int64_t T, const int32_t *seq_lens, int G, int bits, const uint16_t *W_kv, float scale, int S,
+                           int k, float *acc, int64_t acc_stride, uint8_t *qbuf, float *sig, float *part, uint32_t *err,
+                           uint32_t stall_ns, void *const *prof, cudaStream_t st);
 cudaError_t launch_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,
                              int64_t ldqo, const uint16_t *k, int64_t ldk, int n_k, const uint16_t *k_gain,
                              uint16_t *k_out, int64_t ldko, int64_t n_tok, const int32_t *positions, int64_t pos0,
@@ -289,6 +296,54 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
   return FSQ_OK;
 }
 
+// Attention weights: splits and workspace.
+struct WeightsPlan {
+  int levels, S, k;  // splits per row, tiles per split
+  size_t off_q, off_sig, off_part, total;
+};
+
+fsq_status plan_weights(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G, const fsq_attn_opts &op,
+                        WeightsPlan *p) {
+  if (B < 0 || T < 1 || n_q < 1 || n_kv < 1 || d_h < 1 || G < 2) return FSQ_ERR_INVALID_ARG;
+  if (n_q % n_kv) return FSQ_ERR_INVALID_ARG;
+  if (op.variant < FSQ_VARIANT_AUTO || op.variant > FSQ_VARIANT_HYBRID || op.num_splits < 0) return FSQ_ERR_INVALID_ARG;
+  if (op.rope_knorm != 0 && op.rope_knorm != 1) return FSQ_ERR_INVALID_ARG;
+  const int L = levels_of(op.levels);
+  if (!L || !width_ok(G, L) || d_h != FSQ_HEAD_DIM || !weights_supported(n_q, G, bits_of_levels(L)))
+    return FSQ_ERR_UNSUPPORTED;
+  if (op.rope_knorm || op.variant > FSQ_VARIANT_ABSORBED || B > kMaxGridRows) return FSQ_ERR_UNSUPPORTED;
+  const int bits = bits_of_levels(L);
+  if (T > ((int64_t)1 << 37) / (G * bits / 8 > 0 ? G * bits / 8 : 1)) return FSQ_ERR_UNSUPPORTED;
+  const int64_t nt = (T + weights_tile_tokens() - 1) / weights_tile_tokens(), Bc = B > 0 ? B : 1;
+  if (nt > INT32_MAX / 2) return FSQ_ERR_UNSUPPORTED;
+  int64_t k = 0;
+  if (op.num_splits > 0) {
+    const int64_t s = op.num_splits < nt ? op.num_splits : nt;
+    k = (nt + s - 1) / s;
+  } else {
+    // one CTA per SM runs at a time; a CTA costs its tiles and the start and end of about four
+    int64_t best = 0;
+    for (int s = 1; s <= kNumSMs; ++s) {
+      const int64_t kk = (nt + s - 1) / s, ctas = Bc * ((nt + kk - 1) / kk);
+      const int64_t cost = (ctas + kNumSMs - 1) / kNumSMs * (kk + 4);
+      if (s == 1 || cost < best) best = cost, k = kk;
+      if (kk == 1) break;
+    }
+  }
+  p->levels = L;
+  p->k = (int)k;
+  p->S = (int)((nt + k - 1) / k);
+  size_t off = kWsHeader;
+  p->off_q = off;
+  off = align_up(off + weights_query_bytes(n_q, G, bits) * (size_t)Bc, 256);
+  p->off_sig = off;
+  off = align_up(off + sizeof(float) * (size_t)Bc * n_q, 256);
+  p->off_part = off;
+  off = align_up(off + 2 * sizeof(float) * (size_t)Bc * p->S * n_q, 256);
+  p->total = off;
+  return FSQ_OK;
+}
+
 fsq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FSQ_OK : FSQ_ERR_CUDA; }
 
 }  // namespace
@@ -496,6 +551,40 @@ fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q, int d_h
                                  p.Sp, p.Ss, p.k, (uint8_t *)(ws + p.off_q), (float *)(ws + p.off_sig),
                                  (float *)(ws + p.off_part), (uint32_t *)ws, ms, o, op.out_fp32, op.debug_stall_ns,
                                  op.prof_events, (cudaStream_t)stream));
+}
+
+size_t fsq_attn_weights_workspace_size(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G,
+                                       const fsq_attn_opts *opts) {
+  fsq_attn_opts op;
+  if (opts) op = *opts;
+  else fsq_attn_opts_default(&op);
+  WeightsPlan p;
+  return plan_weights(B, T, n_q, n_kv, d_h, G, op, &p) == FSQ_OK ? p.total : 0;
+}
+
+fsq_status fsq_attn_weights(const uint16_t *q, int64_t B, int n_q, int d_h, const uint8_t *codes,
+                            int64_t code_batch_stride_bytes, int64_t T, int G, const uint16_t *W_kv, int n_kv,
+                            const fsq_attn_opts *opts, float *acc, int64_t acc_stride, void *workspace,
+                            size_t workspace_bytes, fsq_stream_t stream) {
+  fsq_attn_opts op;
+  if (opts) op = *opts;
+  else fsq_attn_opts_default(&op);
+  WeightsPlan p;
+  const fsq_status st = plan_weights(B, T, n_q, n_kv, d_h, G, op, &p);
+  if (st != FSQ_OK) return st;
+  if (B == 0) return FSQ_OK;
+  if (!q || !codes || !W_kv || !acc) return FSQ_ERR_INVALID_ARG;
+  const int bits = bits_of_levels(p.levels);
+  if (code_batch_stride_bytes < T * ((int64_t)G * bits / 8) || acc_stride < T) return FSQ_ERR_INVALID_ARG;
+  if (!aligned16(codes) || code_batch_stride_bytes % 16 || !aligned16(q) || !aligned16(W_kv)) return FSQ_ERR_MISALIGNED;
+  if (((uintptr_t)op.seq_lens | (uintptr_t)acc) & 3u) return FSQ_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < p.total) return FSQ_ERR_WORKSPACE;
+  if ((uintptr_t)workspace & 255u) return FSQ_ERR_MISALIGNED;
+  char *ws = (char *)workspace;
+  return from_cuda(launch_weights(q, B, n_q, n_kv, codes, code_batch_stride_bytes, T, op.seq_lens, G, bits, W_kv,
+                                  op.scale > 0.f ? op.scale : 1.f / sqrtf((float)d_h), p.S, p.k, acc, acc_stride,
+                                  (uint8_t *)(ws + p.off_q), (float *)(ws + p.off_sig), (float *)(ws + p.off_part),
+                                  (uint32_t *)ws, op.debug_stall_ns, op.prof_events, (cudaStream_t)stream));
 }
 
 fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint16_t *q_gain, uint16_t *q_out,

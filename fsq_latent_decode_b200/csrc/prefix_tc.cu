@@ -37,6 +37,7 @@
 // of a row's accumulator is decided by the two warps that hold its row.
 // Every wait is bounded (FSQ_ERR_TIMEOUT), as in the other decode kernels.
 #include "common.cuh"
+#include "f16_codes.cuh"
 #include "tc_decode.cuh"
 #include "tc_ptx.cuh"
 
@@ -108,77 +109,6 @@ struct Misc {
   float mx[2][kRows];
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
-
-// A ring position: slot and the parity of its current round.
-struct Ring {
-  int slot = 0;
-  uint32_t par = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++slot == n) {
-      slot = 0;
-      par ^= 1u;
-    }
-  }
-};
-
-// Descriptor of a 128-byte-swizzled operand.  K-major: atoms of 8 rows are
-// 1024 bytes apart (sbo; lbo unused).  MN-major: atoms of 64 MN-coordinates are
-// `lbo` apart, groups of 8 along K 1024 bytes.
-__device__ __forceinline__ uint64_t desc_swz(uint32_t saddr, uint32_t lbo) {
-  return smem_desc(saddr, lbo, 1024) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t m, uint32_t a) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m),
-                            *reinterpret_cast<const __half2 *>(&a));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-// fp16 pairs as constants
-constexpr uint32_t kOne = 0x3C003C00u;
-template <int BITS>
-__host__ __device__ constexpr int order_of(int c) {  // physical place of coordinate c in its group of 8
-  return BITS == 8 ? c : (c & 3) * 2 + (c >> 2);
-}
-
-// Eight codes -> four words of fp16 levels in physical order.  BITS = 8: w and
-// w2 hold codes 0-3 and 4-7; 4: w holds all; 2: the low 16 bits of w.
-template <int BITS>
-__device__ __forceinline__ uint4 levels8(uint32_t w, uint32_t w2) {
-  constexpr uint32_t M = 0x64006400u;  // 1024.0, whose last mantissa bits take the code
-  if constexpr (BITS == 8) {
-    constexpr uint32_t kOff = 0xE480E480u;  // -1152 = -(1024 + 128)
-    return make_uint4(hfma2(__byte_perm(w, M, 0x7150), kOne, kOff), hfma2(__byte_perm(w, M, 0x7352), kOne, kOff),
-                      hfma2(__byte_perm(w2, M, 0x7150), kOne, kOff), hfma2(__byte_perm(w2, M, 0x7352), kOne, kOff));
-  } else if constexpr (BITS == 4) {
-    const uint32_t v = w >> 8;
-    // codes at bit 0: 1024 + n - 1032; at bit 4: (1024 + 16 n) / 16 - 72
-    return make_uint4(hfma2((w & 0x000F000Fu) | M, kOne, 0xE408E408u), hfma2((w & 0x00F000F0u) | M, 0x2C002C00u, 0xD480D480u),
-                      hfma2((v & 0x000F000Fu) | M, kOne, 0xE408E408u), hfma2((v & 0x00F000F0u) | M, 0x2C002C00u, 0xD480D480u));
-  } else {
-    const uint32_t v = (w & 0xFFFFu) | (w << 8);  // codes 4-7 beside codes 0-3, 16 bits up
-    // code k at bit 2k: (1024 + 4^k n) / 4^k - (1024 / 4^k + 2)
-    return make_uint4(hfma2((v & 0x00030003u) | M, kOne, 0xE402E402u), hfma2((v & 0x000C000Cu) | M, 0x34003400u, 0xDC08DC08u),
-                      hfma2((v & 0x00300030u) | M, 0x2C002C00u, 0xD420D420u), hfma2((v & 0x00C000C0u) | M, 0x24002400u, 0xCC80CC80u));
-  }
-}
-
-// Group u of a token (8 codes, BITS bytes) at `row` in shared memory, any alignment of the row
-template <int BITS>
-__device__ __forceinline__ uint4 group8(const uint8_t *row, int u, int align) {
-  const uint8_t *p = row + u * BITS;
-  uint32_t w[2] = {0u, 0u};
-  if (align >= 4 && BITS >= 4) {
-#pragma unroll
-    for (int i = 0; i < BITS / 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
-  } else if (align >= 2) {
-#pragma unroll
-    for (int i = 0; i < BITS / 2; ++i) w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * i) << (16 * (i & 1));
-  } else {
-#pragma unroll
-    for (int i = 0; i < BITS; ++i) w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
-  }
-  return levels8<BITS>(w[0], w[1]);
-}
 
 // 16-byte chunk c (8 coordinates) of token row t in the swizzled atoms
 __device__ __forceinline__ uint32_t z_at(int t, int c) {
@@ -275,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     Ring c;
     for (int i = 0; i < n_tiles; ++i, c.next(stages)) {
       const int st = c.slot;
-      if (!wait_bar(&ms.empty[st], c.par ^ 1u, abort, kWaitNs)) {
+      if (!warp_wait(&ms.empty[st], c.par ^ 1u, abort, kWaitNs)) {
         ok = false;
         break;
       }
@@ -308,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     Ring zs, zp, ss, sp, old;  // tile and S buffer of the next scores; of the next pooling; tile whose S is overwritten
     auto scores = [&](int i) -> bool {
       if (i >= ns) {  // this S buffer holds P(i - ns): its pooling must be done
-        if (!wait_bar(&ms.z_free[old.slot], old.par, abort, kWaitNs)) return false;
+        if (!warp_wait(&ms.z_free[old.slot], old.par, abort, kWaitNs)) return false;
         old.next(nz);
       }
-      if (!wait_bar(&ms.z_ready[zs.slot], zs.par, abort, kWaitNs)) return false;
+      if (!warp_wait(&ms.z_ready[zs.slot], zs.par, abort, kWaitNs)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t d = tm + pl.col_s + ss.slot * kTile, a = tm + pl.col_q;
@@ -326,10 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       ss.next(ns);
       return true;
     };
-    bool ok = wait_bar(&ms.q_ready, 0, abort, kWaitNs) && scores(0);
+    bool ok = warp_wait(&ms.q_ready, 0, abort, kWaitNs) && scores(0);
     for (int i = 0; ok && i < n_tiles; ++i) {
       if (i + 1 < n_tiles) ok = scores(i + 1);
-      ok = ok && wait_bar(&ms.p_ready[sp.slot], sp.par, abort, kWaitNs);
+      ok = ok && warp_wait(&ms.p_ready[sp.slot], sp.par, abort, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
@@ -360,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     }
     Ring cr, zr;
     for (int i = 0; i < n_tiles; ++i, cr.next(stages), zr.next(nz)) {
-      if (!wait_bars(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
+      if (!warp_wait(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
         if (lane == 0) fail();
         break;
       }
@@ -435,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       if (lane == 0) mbar_arrive(&ms.q_ready);
     }
     // test-only stall: a wait that runs out on purpose (nothing completes `never`)
-    if (p.stall_ns != 0u && !wait_bar(&ms.never, 0, abort, p.stall_ns)) ok = false;
+    if (p.stall_ns != 0u && !warp_wait(&ms.never, 0, abort, p.stall_ns)) ok = false;
     float m = -INFINITY, l = 0.f;
     Ring sr, zo;  // S buffer of the tile; tile before it
     for (int i = 0; i < n_tiles; ++i, sr.next(ns)) {
-      ok = ok && wait_bar(&ms.s_full[sr.slot], sr.par, abort, kWaitNs);
+      ok = ok && warp_wait(&ms.s_full[sr.slot], sr.par, abort, kWaitNs);
       tc_fence_after();
       uint32_t s[32];
       float top = -INFINITY;
@@ -475,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
         m = mn;
         if (i > 0 && busy) {
           // O holds every earlier tile once the last pooling is done
-          if (!wait_bar(&ms.z_free[zo.slot], zo.par, abort, kWaitNs)) ok = false;
+          if (!warp_wait(&ms.z_free[zo.slot], zo.par, abort, kWaitNs)) ok = false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 16 * wg; c < Gp; c += 32) {  // the warps take turns at 16 columns
@@ -513,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     // ---- epilogue: O through shared memory (the tiles are spent) to the partials
     if (ok) {
       const int z = (n_tiles - 1) % nz;
-      ok = wait_bar(&ms.z_free[z], (uint32_t)((n_tiles - 1) / nz) & 1u, abort, kWaitNs);
+      ok = warp_wait(&ms.z_free[z], (uint32_t)((n_tiles - 1) / nz) & 1u, abort, kWaitNs);
     }
     if (!ok) fail();
     ms.mx[wg][r] = l;

@@ -304,6 +304,29 @@ FSQ_API fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q,
                                           int n_kv, const fsq_attn_opts *opts, void *workspace,
                                           size_t workspace_bytes, void *o, fsq_stream_t stream);
 
+/* Attention weight of every cached token, summed over the query heads and added
+ * to a running total, for a decode step's queries (what fsq_cache_evict ranks
+ * tokens by):
+ *   acc[b][t] += sum_h softmax_t(scale * q_h . W_k^(j) z_t),  t < L_b (T, or seq_lens[b])
+ *  acc        fp32 [B][T..], acc_stride elements between rows; entries at and
+ *             behind L_b are left alone                          — read, written
+ *  q, codes, W_kv, opts, workspace (fsq_attn_weights_workspace_size): as in
+ *  fsq_decode_attn, except that q is read after the kernels before it and W_v is
+ *  not read; keys are W_k z_t (variant AUTO or ABSORBED, rope_knorm 0; others
+ *  return FSQ_ERR_UNSUPPORTED), out_fp32 is not looked at.
+ * Scores and sums are exact to fp32 (Q' is held in 22 bits).  A call whose first
+ * pass gives up a bounded wait (FSQ_ERR_TIMEOUT) adds nothing; one that gives up
+ * later leaves acc undefined.
+ * Needs: d_h == 128, n_q % n_kv == 0, n_q <= 64, the G rules of the append, acc
+ * 4-byte aligned, acc_stride >= T, T >= 1, T * R <= 2^37, B <= 65535.  B == 0 is
+ * a no-op. */
+FSQ_API size_t fsq_attn_weights_workspace_size(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G,
+                                               const fsq_attn_opts *opts);
+FSQ_API fsq_status fsq_attn_weights(const uint16_t *q, int64_t B, int n_q, int d_h, const uint8_t *codes,
+                                    int64_t code_batch_stride_bytes, int64_t T, int G, const uint16_t *W_kv, int n_kv,
+                                    const fsq_attn_opts *opts, float *acc, int64_t acc_stride, void *workspace,
+                                    size_t workspace_bytes, fsq_stream_t stream);
+
 /* Head norms with rotary positions: queries, and keys that a caller forms
  * itself, as the attention calls with rope_knorm expect them (the same map they
  * apply to the keys they rebuild, [S] eq. 5), in one pass:

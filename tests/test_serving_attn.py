@@ -237,3 +237,203 @@ def test_prefix_captured_and_on_another_stream():
     assert torch.equal(call(torch.empty_like(out)), replayed)
     want = _ref(-q, prefix, codes, W, 8, 256, 16, 100, [1, 100, 50, 0])
     assert (np.abs(replayed.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + TOL * np.abs(want).max()).all()
+
+
+# ---------------------------------------------------------------- attention weights
+# Relative error of one weight, by the size of the largest score s (log2 units):
+# the tensor core adds a score up in at most 36 steps (G = 576), each truncated to
+# an fp32 of at most |s|, 2^-23 |s|: 36 2^-23 |s|, 6.9e-5 at 16; the log-sum-exp
+# carries the same; times ln 2: 9.5e-5 in the worst case at |s| = 16.  Q' (22 bits,
+# fp32 sums of 128), ex2 and the sums add below 1e-6 |s|.  So 1e-4 max(1, |s| / 16).
+def _weights_case(B, n_q, n_kv, G, L, T, seed, q_scale=1.0):
+    codes = oracle_cache(B, T, G, seed, levels=L)
+    W, q = decoder_weights(n_q, n_kv, G, B, seed + 1, levels=L)
+    return codes, W, (q.float() * q_scale).to(torch.bfloat16)
+
+
+def _check_weights(q, codes, W, n_kv, G, L, T, lens=None, **kw):
+    B, n_q = q.shape[:2]
+    r = np.random.default_rng(T + G)
+    acc0 = (r.exponential(size=(B, T + 5)) * n_q / T).astype(np.float32)
+    acc0[:, ::4] = 0.0
+    acc = _dev(acc0)
+    ws = F.Workspace()
+    o = F.attn_opts(seq_lens=None if lens is None else _dev(torch.tensor(lens, dtype=torch.int32)), levels=L, **kw)
+    got = F.attn_weights(_dev(q), _dev(codes), _dev(W), acc, T, n_kv, G, opts=o, workspace=ws)
+    assert got.data_ptr() == acc.data_ptr() and F.workspace_status(ws.buf) == F.FSQ_OK
+    w = O.attn_weights(q.float().numpy(), codes[:, :T], W.float().numpy(), n_kv, G, lengths=lens, levels=L)
+    top = 0.0
+    Wk, _ = O.split_wkv(W.float().numpy(), n_kv, 128)
+    for b in range(B):
+        z = O.unpack(codes[b, :T], G, L).astype(np.float64)
+        for h in range(n_q):
+            top = max(top, np.abs(z @ (Wk[h // (n_q // n_kv)].T @ q[b, h].double().numpy())).max() / math.sqrt(128) * 1.4427)
+    got = got.double().cpu().numpy()
+    n = [T] * B if lens is None else lens
+    for b in range(B):
+        assert np.array_equal(got[b, n[b]:], acc0[b, n[b]:])  # behind the last token nothing moves
+        ref = w[b, :n[b]] + acc0[b, :n[b]]
+        # the last addition rounds once more
+        assert (np.abs(got[b, :n[b]] - ref) <= 1e-4 * max(1.0, top / 16) * w[b, :n[b]] + 2.0 ** -23 * ref + 1e-37).all()
+
+
+W_SHAPES = [(2, 16, 8, 256, 16), (3, 32, 8, 256, 16), (5, 32, 8, 84, 16), (2, 64, 8, 160, 16), (2, 8, 8, 288, 16),
+            (3, 1, 1, 6, 16), (2, 12, 4, 44, 16), (2, 40, 8, 576, 16), (1, 64, 8, 576, 16), (2, 24, 3, 96, 16),
+            (3, 32, 8, 80, 256), (2, 16, 8, 256, 256), (2, 48, 8, 144, 256), (1, 64, 4, 576, 256), (2, 16, 8, 10, 256),
+            (2, 16, 8, 560, 256), (3, 32, 8, 320, 4), (2, 32, 8, 576, 4), (2, 16, 8, 64, 4), (2, 16, 8, 4, 4),
+            (2, 16, 8, 20, 4)]
+
+
+@pytest.mark.parametrize("T", [1, 128, 300, 1111])
+@pytest.mark.parametrize("B,n_q,n_kv,G,L", W_SHAPES)
+def test_weights_parity(B, n_q, n_kv, G, L, T):
+    codes, W, q = _weights_case(B, n_q, n_kv, G, L, T, seed=500 + G + T)
+    lens = None if T < 300 else [max(1, T - 256 * b - 43 * (b > 0)) for b in range(B)]
+    _check_weights(q, codes, W, n_kv, G, L, T, lens)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 9, 1000])
+def test_weights_split_counts(splits):
+    codes, W, q = _weights_case(3, 32, 8, 256, 16, 4000, seed=71)
+    _check_weights(q, codes, W, 8, 256, 16, 4000, [4000, 1, 2049], num_splits=splits)
+
+
+@pytest.mark.parametrize("G,L", [(256, 16), (84, 16), (144, 256), (320, 4)])
+@pytest.mark.parametrize("q_scale", [0.0, 5.0, 60.0])
+def test_weights_softmax_corners(q_scale, G, L):
+    """Equal scores; sharp ones; ones that spread over thousands of powers of two,
+    so that the first token's score is far below the largest."""
+    codes, W, q = _weights_case(2, 32, 8, G, L, 1500, seed=80 + G, q_scale=q_scale)
+    _check_weights(q, codes, W, 8, G, L, 1500, num_splits=2)
+
+
+def test_weights_of_many_rows_and_a_long_row():
+    codes, W, q = _weights_case(200, 16, 8, 84, 16, 200, seed=90)
+    _check_weights(q, codes, W, 8, 84, 16, 200)
+    codes, W, q = _weights_case(1, 16, 8, 256, 16, 40000, seed=91)
+    _check_weights(q, codes, W, 8, 256, 16, 40000)
+
+
+def test_weights_accumulate_over_steps_and_ignore_what_lies_behind():
+    """Several steps on one workspace add up; bytes behind a row's length change nothing."""
+    B, T, G = 2, 700, 84
+    codes, W, q = _weights_case(B, 32, 8, G, 16, T, seed=95)
+    lens = [700, 333]
+    outs = []
+    for fill in (0, 255):
+        c = codes.copy()
+        c[1, 333:] = fill
+        acc, ws = torch.zeros((B, T), device=DEV), F.Workspace()
+        o = F.attn_opts(seq_lens=_dev(torch.tensor(lens, dtype=torch.int32)))
+        for step in range(3):
+            F.attn_weights(_dev(torch.roll(q, step, 1)), _dev(c), _dev(W), acc, T, 8, G, opts=o, workspace=ws)
+        outs.append(acc)
+    assert torch.equal(*outs)
+    total = outs[0].double().sum(1).cpu().numpy()
+    assert np.allclose(total, 3 * 32, rtol=1e-5)  # every head of every step spends a weight of 1
+
+
+def test_weights_bounded_wait_adds_nothing_and_next_call_recovers():
+    codes, W, q = _weights_case(2, 32, 8, 256, 16, 3000, seed=97)
+    acc, ws = torch.zeros((2, 3000), device=DEV), F.Workspace()
+    a = (_dev(q), _dev(codes), _dev(W), acc, 3000, 8, 256)
+    F.attn_weights(*a, opts=F.attn_opts(debug_stall_ns=2_000_000), workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_ERR_TIMEOUT and (acc == 0).all()
+    F.attn_weights(*a, workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_OK
+    assert np.allclose(acc.double().sum(1).cpu().numpy(), 32, rtol=1e-5)
+
+
+def test_weights_out_of_range_length_and_non_finite_queries():
+    codes, W, q = _weights_case(4, 16, 8, 84, 16, 300, seed=98)
+    q[3, 2, 1] = float("nan")
+    acc, ws = torch.zeros((4, 300), device=DEV), F.Workspace()
+    o = F.attn_opts(seq_lens=_dev(torch.tensor([301, 0, 299, 300], dtype=torch.int32)))
+    F.attn_weights(_dev(q), _dev(codes), _dev(W), acc, 300, 8, 84, opts=o, workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_ERR_INVALID_ARG
+    want = O.attn_weights(q[:3].float().numpy(), codes[:3, :300], W.float().numpy(), 8, 84, lengths=[300, 1, 299])
+    assert np.allclose(acc[:3].cpu().numpy(), want, rtol=1e-4, atol=1e-37)
+    assert torch.isnan(acc[3]).all()  # the row's sum over heads
+
+
+def test_weights_captured_and_on_another_stream():
+    codes, W, q = _weights_case(3, 32, 8, 256, 16, 1000, seed=99)
+    a = [_dev(x) for x in (q, codes, W)]
+    ws, acc = F.Workspace(), torch.zeros((3, 1000), device=DEV)
+    want = F.attn_weights(*a, torch.zeros_like(acc), 1000, 8, 256, workspace=ws).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        F.attn_weights(*a, acc, 1000, 8, 256, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(acc, want)
+    acc.zero_()
+    g = torch.cuda.CUDAGraph()
+    o = F.attn_opts()
+    with torch.cuda.graph(g):
+        F.attn_weights(*a, acc, 1000, 8, 256, opts=o, workspace=ws)
+    acc.zero_()
+    g.replay()
+    assert torch.equal(acc, want)
+    g.replay()
+    assert torch.equal(acc, want + want)
+
+
+# ---------------------------------------------------------------- the operators together
+def test_serving_run():
+    """A batch on one prompt: decode steps on the shared prefix with queries normed
+    and rotated in place, then the rows' caches put together, weights gathered over
+    steps, the caches cut to a budget in place, and decoding goes on in them."""
+    B, n_q, n_kv, G, C, Tp, T = 3, 32, 8, 256, 1024, 500, 6
+    r = np.random.default_rng(0)
+    bf = lambda a: torch.from_numpy(np.asarray(a, np.float32)).to(torch.bfloat16)  # noqa: E731
+    prefix = oracle_cache(1, Tp, G, 77)[0, :Tp]
+    W, _ = decoder_weights(n_q, n_kv, G, B, 78)
+    E = bf(r.normal(size=(G, C)) * 2 / math.sqrt(C))
+    gain = bf(1 + 0.1 * r.normal(size=128))
+    own = torch.zeros((B, 16, 128), dtype=torch.uint8, device=DEV)
+    ws = F.Workspace()
+    dp, dW = _dev(prefix), _dev(W)
+    for t in range(T):  # every step appends a token to each row and attends
+        F.append_rows(_dev(bf(r.normal(size=(B, C)))), _dev(E), own, t)
+        q = bf(r.normal(size=(B, n_q, 128)))
+        dq = _dev(q)
+        pos = torch.full((B,), Tp + t + 1, dtype=torch.int32, device=DEV)
+        F.qk_norm_rope(dq, q_gain=_dev(gain), positions=pos, pos0=-1, q_out=dq)
+        got = F.decode_attn_prefix(dq, dp, own, dW, Tp, t + 1, n_kv, G, opts=F.attn_opts(out_fp32=True), workspace=ws)
+        want = _ref(dq.cpu(), prefix, own.cpu().numpy(), W, n_kv, G, 16, t + 1)
+        assert rel_err(got.cpu().numpy(), want) <= TOL
+    n = Tp + T
+    cache = torch.zeros((B, 512, 128), dtype=torch.uint8, device=DEV)
+    cache[:, :Tp], cache[:, Tp:n] = dp, own[:, :T]
+    acc, lens = torch.zeros((B, 512), device=DEV), torch.tensor([n, n - 7, n - 100], dtype=torch.int32, device=DEV)
+    ref, before = np.zeros((B, 512)), cache.cpu().numpy()
+    for _ in range(4):
+        q = bf(r.normal(size=(B, n_q, 128)))
+        F.attn_weights(_dev(q), cache, dW, acc, n, n_kv, G, opts=F.attn_opts(seq_lens=lens), workspace=ws)
+        ref[:, :n] += O.attn_weights(q.float().numpy(), before[:, :n], W.float().numpy(), n_kv, G, lengths=lens.tolist())
+    assert np.allclose(acc.cpu().numpy(), ref, rtol=2e-4, atol=1e-30)
+    keep = 410
+    a = acc.cpu().numpy()
+    kept = torch.empty((B, keep), dtype=torch.int32, device=DEV)
+    F.cache_evict(cache, acc, n, keep, 32, G=G, seq_lens=lens, lens_out=lens, kept=kept, workspace=ws)
+    rows = []
+    for b, old in enumerate([n, n - 7, n - 100]):
+        at = O.evict(a[b], old, keep, 32)
+        assert kept[b, :len(at)].tolist() == at.tolist()
+        rows.append(before[b, at])
+    assert lens.tolist() == [410, 410, 406]
+    assert (acc[:2, keep:] == 0).all()
+    q = bf(r.normal(size=(B, n_q, 128)))
+    got = F.decode_attn(_dev(q), cache, dW, keep, n_kv, G, opts=F.attn_opts(out_fp32=True, seq_lens=lens), workspace=ws)
+    want = np.concatenate([O.decode_attn(q[b:b + 1].float().numpy(), rows[b][None], W.float().numpy(), n_kv, G)
+                           for b in range(B)])
+    assert rel_err(got.cpu().numpy(), want) <= TOL
+    # the keys that the hybrid form rebuilds are normed and rotated by their place in the cut cache
+    o = F.attn_opts(variant="hybrid", rope_knorm=True, out_fp32=True, seq_lens=lens)
+    dq = F.qk_norm_rope(_dev(q), positions=lens, pos0=-1)
+    got = F.decode_attn(dq, cache, dW, keep, n_kv, G, opts=o, workspace=ws)
+    rk = dict(gain=np.ones(128), eps=1e-6, base=1e6)
+    want = np.concatenate([O.decode_attn(dq[b:b + 1].float().cpu().numpy(), rows[b][None], W.float().numpy(), n_kv, G,
+                                         rope_knorm=rk) for b in range(B)])
+    assert rel_err(got.cpu().numpy(), want) <= TOL

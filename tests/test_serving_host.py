@@ -128,3 +128,100 @@ def test_evict_oracle():
     assert O.evict(a, 6, 3, 3).tolist() == [3, 4, 5]
     assert O.evict(a, 7, 1, 0).tolist() == [4]
     assert O.evict([math.nan, -math.inf, -1.0, 0.0], 4, 3, 0).tolist() == [1, 2, 3]
+
+
+# ---------------------------------------------------------------- shared-prefix attention, attention weights
+def _prefix(**kw):
+    a = dict(q=1 << 20, B=3, n_q=32, d=128, prefix=2 << 20, Tp=100, codes=3 << 20, bs=12800, T=100, G=256, W=4 << 20,
+             n_kv=8, opts=F.attn_opts(), ws=5 << 20, wsb=1 << 40, o=6 << 20, stream=None)
+    a.update(kw)
+    return F.decode_attn_prefix_raw(*a.values())
+
+
+def _weights(**kw):
+    a = dict(q=1 << 20, B=3, n_q=32, d=128, codes=3 << 20, bs=12800, T=100, G=256, W=4 << 20, n_kv=8,
+             opts=F.attn_opts(), acc=7 << 20, acs=100, ws=5 << 20, wsb=1 << 40, stream=None)
+    a.update(kw)
+    return F.attn_weights_raw(*a.values())
+
+
+def test_prefix_refusals():
+    bad, un, mis = F.FSQ_ERR_INVALID_ARG, F.FSQ_ERR_UNSUPPORTED, F.FSQ_ERR_MISALIGNED
+    assert _prefix(B=0, q=None, prefix=None) == F.FSQ_OK
+    for kw in (dict(B=-1), dict(Tp=0), dict(T=-1), dict(n_q=12), dict(n_q=0), dict(q=None), dict(prefix=None),
+               dict(codes=None), dict(W=None), dict(o=None), dict(bs=12784), dict(opts=F.attn_opts(num_splits=-1)),
+               dict(opts=F.attn_opts(variant=7))):
+        assert _prefix(**kw) == bad, kw
+    for kw in (dict(d=64), dict(G=255), dict(G=258), dict(n_q=136), dict(B=65536), dict(Tp=1 << 40),
+               dict(opts=F.attn_opts(rope_knorm=True)), dict(opts=F.attn_opts(variant="expand")),
+               dict(opts=F.attn_opts(variant="hybrid")), dict(opts=F.attn_opts(levels=8))):
+        assert _prefix(**kw) == un, kw
+    lens = F.attn_opts()
+    lens.seq_lens = 18
+    for kw in (dict(q=(1 << 20) + 2), dict(prefix=(2 << 20) + 8), dict(codes=(3 << 20) + 8), dict(bs=12808),
+               dict(W=(4 << 20) + 2), dict(o=(6 << 20) + 4), dict(ws=(5 << 20) + 128), dict(opts=lens)):
+        assert _prefix(**kw) == mis, kw
+    need = F.prefix_workspace_size(3, 100, 100, 32, 8, 128, 256)
+    assert need > 0 and need % 256 == 0
+    assert _prefix(wsb=need - 1) == F.FSQ_ERR_WORKSPACE and _prefix(ws=None) == F.FSQ_ERR_WORKSPACE
+    assert F.prefix_workspace_size(3, 0, 100, 32, 8, 128, 256) == 0
+    assert F.prefix_workspace_size(3, 100, 0, 128, 8, 128, 256) > 0
+
+
+def test_weights_refusals():
+    bad, un, mis = F.FSQ_ERR_INVALID_ARG, F.FSQ_ERR_UNSUPPORTED, F.FSQ_ERR_MISALIGNED
+    assert _weights(B=0, q=None) == F.FSQ_OK
+    for kw in (dict(B=-1), dict(T=0), dict(n_q=12), dict(q=None), dict(codes=None), dict(W=None), dict(acc=None),
+               dict(bs=12784), dict(acs=99), dict(opts=F.attn_opts(num_splits=-1))):
+        assert _weights(**kw) == bad, kw
+    for kw in (dict(d=64), dict(G=255), dict(G=578), dict(n_q=72), dict(B=65536), dict(T=1 << 40),
+               dict(opts=F.attn_opts(rope_knorm=True)), dict(opts=F.attn_opts(variant="expand")),
+               dict(opts=F.attn_opts(levels=8))):
+        assert _weights(**kw) == un, kw
+    for kw in (dict(q=(1 << 20) + 2), dict(codes=(3 << 20) + 8), dict(bs=12808), dict(W=(4 << 20) + 2),
+               dict(acc=(7 << 20) + 2), dict(ws=(5 << 20) + 128)):
+        assert _weights(**kw) == mis, kw
+    need = F.attn_weights_workspace_size(3, 100, 32, 8, 128, 256)
+    assert need > 0 and _weights(wsb=need - 1) == F.FSQ_ERR_WORKSPACE and _weights(ws=None) == F.FSQ_ERR_WORKSPACE
+    for L, G in ((16, 576), (256, 576), (4, 576), (16, 2)):  # every width, up to 64 heads
+        assert F.attn_weights_workspace_size(3, 100, 64, 8, 128, G, F.attn_opts(levels=L)) > 0
+
+
+def test_attention_wrapper_refusals():
+    q, W = torch.zeros((2, 16, 128), dtype=torch.bfloat16), torch.zeros((2048, 84), dtype=torch.bfloat16)
+    codes, prefix, acc = torch.zeros((2, 32, 42), dtype=torch.uint8), torch.zeros((50, 42), dtype=torch.uint8), torch.zeros(2, 30)
+    for call in (lambda: F.decode_attn_prefix(q, prefix, codes, W, 51, 30, 8, 84),
+                 lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 33, 8, 84),
+                 lambda: F.decode_attn_prefix(q, prefix, None, W, 50, 30, 8, 84),
+                 lambda: F.decode_attn_prefix(q, prefix, codes[:1], W, 50, 30, 8, 84),
+                 lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 30, 4, 84),
+                 lambda: F.decode_attn_prefix(q.float(), prefix, codes, W, 50, 30, 8, 84),
+                 lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 30, 8, 84, out=torch.zeros(2, 16, 128)),
+                 lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 30, 8, 84),
+                 lambda: F.attn_weights(q, codes, W, acc, 31, 8, 84), lambda: F.attn_weights(q, codes, W, acc.T, 30, 8, 84),
+                 lambda: F.attn_weights(q, codes[:1], W, acc, 30, 8, 84),
+                 lambda: F.attn_weights(q[:, :, :64], codes, W, acc, 30, 8, 84),
+                 lambda: F.attn_weights(q, codes, W, acc.double(), 30, 8, 84),
+                 lambda: F.attn_weights(q, codes, W, acc, 30, 8, 84)):  # the last of each: not on a GPU
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_attention_oracles():
+    r = np.random.default_rng(3)
+    B, n_q, n_kv, G, Tp, T = 2, 4, 2, 8, 9, 5
+    prefix, codes = r.integers(0, 256, (Tp, G // 2), dtype=np.uint8), r.integers(0, 256, (B, T, G // 2), dtype=np.uint8)
+    W, q = r.normal(size=(2 * n_kv * 128, G)), r.normal(size=(B, n_q, 128))
+    got = O.decode_attn_prefix(q, prefix, codes, W, n_kv, G, lengths=[5, 0])
+    # against torch's own attention over the concatenated rows
+    for b, n in enumerate([5, 0]):
+        K, V = O.reconstruct_kv(O.unpack(np.concatenate([prefix, codes[b, :n]]), G), W, n_kv, 128)
+        t = lambda a: torch.from_numpy(a).repeat_interleave(2, 0)  # noqa: E731
+        want = torch.nn.functional.scaled_dot_product_attention(torch.from_numpy(q[b])[:, None], t(K), t(V))[:, 0]
+        assert np.allclose(got[b], want.numpy(), rtol=1e-11)
+    w = O.attn_weights(q, codes, W, n_kv, G, lengths=[5, 3])
+    assert np.allclose(w.sum(1), n_q) and (w[1, 3:] == 0).all()
+    # the weights give the attention back: sum_t w_ht v_t, one head at a time
+    K, V = O.reconstruct_kv(O.unpack(codes[0], G), W, n_kv, 128)
+    one = O.attn_weights(q[:1, :1], codes[:1], np.concatenate([W[:128], W[256:384]]), 1, G)
+    assert np.allclose(one[0] @ V[0], O.decode_attn(q[:1], codes[:1], W, n_kv, G)[0, 0])

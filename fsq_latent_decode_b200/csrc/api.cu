@@ -52,12 +52,13 @@ cudaError_t launch_absorbed_tc(const uint16_t *q, const uint8_t *codes, int64_t 
                                uint32_t stall_ns, void *const *prof, cudaStream_t st);
 bool prefix_supported(int n_q, int G);
 int prefix_rows_per_tile(int n_q);
+int prefix_max_splits();
 int prefix_tile_tokens();
 size_t prefix_query_bytes(int G);
-cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, int d_h, const uint8_t *shared, int64_t Tp,
+cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, const uint8_t *shared, int64_t Tp,
                           const uint8_t *codes, int64_t bstride, int64_t T, const int32_t *seq_lens, int G, int bits,
                           const uint16_t *W_kv, float scale, int QT, int Sp, int Ss, int k, uint8_t *qbuf, float *sig,
-                          float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32, uint32_t stall_ns,
+                          float *part, uint32_t *err, void *o, int out_fp32, uint32_t stall_ns,
                           void *const *prof, cudaStream_t st);
 bool weights_supported(int n_q, int G, int bits);
 int weights_tile_tokens();
@@ -237,8 +238,7 @@ fsq_status plan_decode(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G, 
 // Shared-prefix attention: query tiles, splits, workspace.
 struct PrefixPlan {
   int levels, QT, Sp, Ss, k;  // k: tiles of a split, of the prefix and of a row's own tokens alike
-  MergePlan mp;
-  size_t off_q, off_sig, off_part, off_mslab, off_mcnt, total;
+  size_t off_q, off_sig, off_part, total;
 };
 
 fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int d_h, int G, const fsq_attn_opts &op,
@@ -273,6 +273,8 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
       if (kk == 1) break;
     }
   }
+  // a row's partials fit the merge
+  while ((nt + k - 1) / k + (no + k - 1) / k > prefix_max_splits()) k *= 2;
   const int64_t Sp = (nt + k - 1) / k, Ss = (no + k - 1) / k;
   if (QT * Sp + Bc * Ss > INT32_MAX) return FSQ_ERR_UNSUPPORTED;
   p->levels = L;
@@ -287,11 +289,6 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
   off = align_up(off + sizeof(float) * (size_t)Bc * n_q, 256);
   p->off_part = off;
   off = align_up(off + sizeof(float) * (size_t)Bc * (Sp + Ss) * n_q * (2 + G), 256);
-  p->mp = merge_plan((int)(Sp + Ss), Bc, n_q, n_kv, G);
-  p->off_mslab = off;
-  off = align_up(off + p->mp.slab_bytes, 256);
-  p->off_mcnt = off;
-  off = align_up(off + p->mp.cnt_bytes, 256);
   p->total = off;
   return FSQ_OK;
 }
@@ -544,12 +541,10 @@ fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q, int d_h
   if (!workspace || workspace_bytes < p.total) return FSQ_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255u) return FSQ_ERR_MISALIGNED;
   char *ws = (char *)workspace;
-  MergeScratch ms{nullptr, nullptr, 0};
-  if (p.mp.cnt_bytes) ms = {(float *)(ws + p.off_mslab), (uint32_t *)(ws + p.off_mcnt), (int)(B * n_kv)};
-  return from_cuda(launch_prefix(q, B, n_q, n_kv, d_h, prefix_codes, T_prefix, codes, code_batch_stride_bytes, T,
+  return from_cuda(launch_prefix(q, B, n_q, n_kv, prefix_codes, T_prefix, codes, code_batch_stride_bytes, T,
                                  op.seq_lens, G, bits, W_kv, op.scale > 0.f ? op.scale : 1.f / sqrtf((float)d_h), p.QT,
                                  p.Sp, p.Ss, p.k, (uint8_t *)(ws + p.off_q), (float *)(ws + p.off_sig),
-                                 (float *)(ws + p.off_part), (uint32_t *)ws, ms, o, op.out_fp32, op.debug_stall_ns,
+                                 (float *)(ws + p.off_part), (uint32_t *)ws, o, op.out_fp32, op.debug_stall_ns,
                                  op.prof_events, (cudaStream_t)stream));
 }
 

@@ -33,11 +33,29 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b0, uint32_t p0, uint64_t *b
   return __all_sync(0xffffffffu, wait_bars(b0, p0, b1, p1, abort, limit_ns));
 }
 
-// Descriptor of a 128-byte-swizzled operand.  K-major: atoms of 8 rows are
-// 1024 bytes apart (sbo; lbo unused).  MN-major: atoms of 64 MN-coordinates are
-// `lbo` apart, groups of 8 along K 1024 bytes.
-__device__ __forceinline__ uint64_t desc_swz(uint32_t saddr, uint32_t lbo) {
-  return smem_desc(saddr, lbo, 1024) | ((uint64_t)2 << 61);
+// 128-byte-swizzled operand B of an MMA, as the two words of its descriptor.
+// K-major: atoms of 8 rows are 1024 bytes apart (lbo unused).  MN-major: atoms
+// of 64 MN-coordinates are `lbo` bytes apart, groups of 8 along K 1024 bytes.
+// Moving along the operand adds (bytes / 16) to the low word.
+constexpr uint32_t kSwzHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t swz_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+// D[tmem] (+)= A[tmem] B[smem], run by a whole converged warp and issued by its
+// elected lane (el != 0).  An MMA takes its operands from uniform registers: with
+// the warp converged, constant steps and a base column that is known to be 0, a
+// step costs a few uniform additions and the tensor core runs at its rate (32
+// cycles for N = 64, K = 16; from one diverged lane, with descriptors in ordinary
+// registers, the same loop issued one every 85-180 cycles).
+__device__ __forceinline__ void mma_ts_warp(uint32_t el, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSwzHi), "r"(el)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t m, uint32_t a) {

@@ -38,6 +38,7 @@
 // Every wait is bounded (FSQ_ERR_TIMEOUT), as in the other decode kernels.
 #include "common.cuh"
 #include "f16_codes.cuh"
+#include "query_f16.cuh"
 #include "tc_decode.cuh"
 #include "tc_ptx.cuh"
 
@@ -55,8 +56,14 @@ constexpr int kMaxStages = 6, kMaxZ = 6, kMaxS = 4;
 constexpr int kDqWarps = 4;
 constexpr int kMiscBytes = 2048;
 constexpr size_t kSmemMax = 227 * 1024;
-constexpr float kTau = 8.f;                        // rescale when a score exceeds the running max by 2^8
-constexpr float kLift = 6.f;                       // the running max enters P as 2^6
+// A row's reference m enters P as 2^kLift and moves when a score exceeds it by
+// 2^kTau, so P stays below 2^15 (fp16 ends at 2^16) and weights count down to
+// 2^-26 of the reference.  Random scores climb a few powers of two beyond a
+// tile's first maximum; moving O costs 1.5k cycles of a tile's 1.3k, so the
+// window is as wide as fp16 lets it be (kTau = 8: 97 us at G = 256, 131072
+// shared tokens, 16 rows; 13: see the table).
+constexpr float kTau = 13.f;
+constexpr float kLift = 2.f;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 1000000000ull;
 
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = ms.tmem_base;
+  constexpr uint32_t tm = 0;  // all 512 columns are this CTA's
   pdl_trigger();  // the merge kernel may start staging W_v
   auto fail = [&]() {
     record_error(p.err, FSQ_ERR_TIMEOUT);
@@ -234,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
-    const uint32_t id_s = idesc_f16(kRows, kTile, 0, 0), id_o = idesc_f16(kRows, Gp, 0, 1);
+    constexpr uint32_t id_s = idesc_f16(kRows, kTile, 0, 0);
+    const uint32_t id_o = idesc_f16(kRows, Gp, 0, 1), el = elect_one();
     Ring zs, zp, ss, sp, old;  // tile and S buffer of the next scores; of the next pooling; tile whose S is overwritten
     auto scores = [&](int i) -> bool {
       if (i >= ns) {  // this S buffer holds P(i - ns): its pooling must be done
@@ -243,14 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       }
       if (!warp_wait(&ms.z_ready[zs.slot], zs.par, abort, kWaitNs)) return false;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tm + pl.col_s + ss.slot * kTile, a = tm + pl.col_q;
-        const uint64_t b = desc_swz(z_a + zs.slot * pl.z_bytes, 16);
-#pragma unroll 4
-        for (int k = 0; k < Gp / 16; ++k)
-          mma_ts(d, a + 8 * k, b + (uint64_t)(((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
-        tc_commit(&ms.s_full[ss.slot]);
+      const uint32_t d = tm + pl.col_s + ss.slot * kTile, a = tm + pl.col_q;
+      const uint32_t b = swz_lo(z_a + zs.slot * pl.z_bytes, 16);
+#pragma unroll
+      for (int k = 0; k < kMaxG / 16; ++k) {
+        if (16 * k >= Gp) break;
+        mma_ts_warp(el, d, a + 8 * k, b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
       }
+      if (el) tc_commit(&ms.s_full[ss.slot]);
       __syncwarp();
       zs.next(nz);
       ss.next(ns);
@@ -262,14 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       ok = ok && warp_wait(&ms.p_ready[sp.slot], sp.par, abort, kWaitNs);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t a = tm + pl.col_s + sp.slot * kTile;
-        const uint64_t b = desc_swz(z_a + zp.slot * pl.z_bytes, kAtomBytes);
+      const uint32_t a = tm + pl.col_s + sp.slot * kTile;
+      const uint32_t b = swz_lo(z_a + zp.slot * pl.z_bytes, kAtomBytes);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tm, a + 8 * k, b + (uint64_t)((k * 2048) >> 4), id_o, (i > 0 || k > 0) ? 1u : 0u);
-        tc_commit(&ms.z_free[zp.slot]);
-      }
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts_warp(el, tm, a + 8 * k, b + ((k * 2048) >> 4), id_o, k > 0 || i > 0 ? 1u : 0u);
+      if (el) tc_commit(&ms.z_free[zp.slot]);
       __syncwarp();
       zp.next(nz);
       sp.next(ns);
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       // half of the row's Q' into TMEM; rows without a query are zero
       const uint8_t *qr = p.qbuf + ((int64_t)qt * p.rpt * p.n_q + r) * (NA * 128);
       if (live) sig = p.sig[(int64_t)qt * p.rpt * p.n_q + r];
-#pragma unroll 1
+#pragma unroll 4
       for (int c = 8 * wg; c < Gp / 2; c += 16) {  // columns: two coordinates each
         uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
         if (live) {
@@ -408,13 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
           if (!warp_wait(&ms.z_free[zo.slot], zo.par, abort, kWaitNs)) ok = false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 16 * wg; c < Gp; c += 32) {  // the warps take turns at 16 columns
-            uint32_t a[16];
+          for (int c = 16 * wg; c < Gp; c += 64) {  // the warps take turns at 16 columns, two turns at once
+            uint32_t a[32];
+            const bool two = c + 32 < Gp;
             tmem_ld16(tm + lanes + c, a);
+            if (two) tmem_ld16(tm + lanes + c + 32, a + 16);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
+            for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
             tmem_st16(tm + lanes + c, a);
+            if (two) tmem_st16(tm + lanes + c + 32, a + 16);
           }
         }
       }
@@ -488,61 +497,142 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
 // Per (kv head j, batch row b): q'_h[g] = c sum_d W_k[j d_h + d][g] q_h[d] (c =
 // scale log2 e), scaled by the power of two that brings the head's largest
 // weight into [1, 2), as a row of fp16 in physical order; sig_h takes the power
-// back.  Also clears the error word and the merge's arrival counts.
+// back.  Also clears the error word.
 template <int BITS>
-__global__ void __launch_bounds__(256) prefix_query(const uint16_t *__restrict__ q, const uint16_t *__restrict__ W_kv,
-                                                    int n_q, int n_kv, int G, int NA, float c,
-                                                    uint8_t *__restrict__ qbuf, float *__restrict__ sig, uint32_t *err,
-                                                    MergeScratch msc) {
-  constexpr int D = FSQ_HEAD_DIM, kHeads = 4;  // heads worked on together
-  __shared__ float qsm[kHeads][D];
-  __shared__ float red[kHeads][8];
-  const int j = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int grp = n_q / n_kv;
+__global__ void __launch_bounds__(kAbsorbThreads, 1) prefix_query(const uint16_t *__restrict__ q,
+                                                               const uint16_t *__restrict__ W_kv, int n_q, int n_kv,
+                                                               int G, int NA, float c, uint8_t *__restrict__ qbuf,
+                                                               float *__restrict__ sig, uint32_t *err) {
+  __shared__ AbsorbSmem<kMaxG> sm;
+  const int64_t b = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (j == 0 && b == 0) {
-    if (tid == 0) *err = 0u;
-    for (int i = tid; i < msc.ncnt; i += 256) msc.cnt[i] = 0u;
-  }
-  for (int h0 = 0; h0 < grp; h0 += kHeads) {
-    const int nh = min(kHeads, grp - h0);
-    for (int i = tid; i < kHeads * D; i += 256)
-      qsm[i / D][i % D] = i / D < nh ? bf16_to_f32(q[((int64_t)b * n_q + j * grp + h0) * D + i]) : 0.f;
-    __syncthreads();
-    const int g = tid;  // G <= 256
-    float v[kHeads] = {0.f, 0.f, 0.f, 0.f};
-    if (g < G) {
-      const uint16_t *w = W_kv + (int64_t)j * D * G + g;
-#pragma unroll 16
-      for (int d = 0; d < D; ++d) {
-        const float wd = bf16_to_f32(w[(int64_t)d * G]);
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *err = 0u;
+  absorb_heads(
+      sm, q, W_kv, n_q, n_kv, G, NA * kAtom, c, blockIdx.x, b,
+      [&](int h, int g, float v, int e) {
+        reinterpret_cast<__half *>(qbuf)[(b * n_q + h) * (NA * kAtom) + ((g & ~7) | order_of<BITS>(g & 7))] =
+            __float2half_rn(scalbnf(v, -e));
+      },
+      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e); });
+}
+
+// ---------------------------------------------------------------- split merge
+// Per (kv head j, batch row b): the group's heads, four at a time,
+//   m = max_s m_s,  w_s = 2^(m_s - m),  abar_h = sum_s w_s O_s / sum_s w_s l_s,  o_h = W_v^(j) abar_h.
+// A thread sums one coordinate pair of one head over its share of the splits
+// (the loads of eight splits are in flight together); a warp then takes eight
+// rows of W_v, loaded into registers before the wait for the split kernel.
+constexpr int kMergeThreads = 512, kMergeHeads = 4, kMergeRows = FSQ_HEAD_DIM / (kMergeThreads / 32);
+constexpr int kMaxSplits = 2048;  // of a row
+
+// VEC: coordinates a lane reads of a W_v row at once (4, or 2 where G is not a multiple of 4)
+template <int VEC>
+__global__ void __launch_bounds__(kMergeThreads, 1) prefix_merge(const float *__restrict__ part, int S, int n_q, int n_kv,
+                                                              int G, const uint16_t *__restrict__ W_kv, void *o,
+                                                              int out_fp32) {
+  constexpr int D = FSQ_HEAD_DIM, STEPS = kMaxG / (32 * VEC);
+  extern __shared__ __align__(16) float wts[];  // [kMergeHeads][S]: w_s / sum
+  __shared__ float2 sum[kMergeThreads];
+  __shared__ __align__(16) float abar[kMergeHeads][kMaxG];
+  const int j = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t b = blockIdx.y;
+  const int grp = n_q / n_kv;
+  // rows kMergeRows * warp .. of W_v^(j); coordinates 32 VEC i + VEC lane ..
+  uint32_t w[kMergeRows][STEPS][VEC / 2];
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) v[k] = fmaf(wd, qsm[k][d], v[k]);
+  for (int r = 0; r < kMergeRows; ++r)
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int g = 32 * VEC * i + VEC * lane;
+      const uint16_t *src = W_kv + ((int64_t)(n_kv + j) * D + warp * kMergeRows + r) * G + g;
+      if constexpr (VEC == 4) {
+        const uint2 v = g < G ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
+        w[r][i][0] = v.x, w[r][i][1] = v.y;
+      } else {
+        w[r][i][0] = g < G ? *reinterpret_cast<const uint32_t *>(src) : 0u;
       }
     }
+  pdl_wait();
+  const int64_t hs = 2 + G, ss = (int64_t)n_q * hs;  // floats of a record, of a split
+  for (int h0 = 0; h0 < grp; h0 += kMergeHeads) {
+    const int nh = min(kMergeHeads, grp - h0);
+    const float *rec = part + (b * S * n_q + (int64_t)j * grp + h0) * hs;
+    if (warp < nh) {  // a warp per head: the splits' weights
+      float m = -INFINITY, l = 0.f;
+      for (int s = lane; s < S; s += 32) m = fmaxf(m, rec[s * ss + warp * hs]);
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-      v[k] *= c;
-      float a = fabsf(v[k]);
+      for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      for (int s = lane; s < S; s += 32) {
+        const float2 ml = *reinterpret_cast<const float2 *>(rec + s * ss + warp * hs);
+        const float e = exp2f(ml.x - m);  // 0 for an empty split
+        wts[warp * S + s] = e;
+        l = fmaf(e, ml.y, l);
+      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      if ((tid & 31) == 0) red[k][tid >> 5] = a;
+      for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      const float inv = 1.f / l;
+      for (int s = lane; s < S; s += 32) wts[warp * S + s] *= inv;
     }
     __syncthreads();
+    const int pairs = G / 2, items = nh * pairs, nsub = min(16, max(1, kMergeThreads / items));
+    {
+      const int it = tid % items, sub = tid / items, h = it / pairs, x = it % pairs;  // items <= 4 * 128
+      float2 a = make_float2(0.f, 0.f);
+      if (sub < nsub) {
+        const float *src = rec + h * hs + 2 + 2 * x;
+#pragma unroll 8
+        for (int s = sub; s < S; s += nsub) {
+          const float2 v = *reinterpret_cast<const float2 *>(src + s * ss);
+          const float e = wts[h * S + s];
+          a.x = fmaf(e, v.x, a.x);
+          a.y = fmaf(e, v.y, a.y);
+        }
+      }
+      if (nsub > 1) {
+        sum[tid] = a;
+        __syncthreads();
+        if (sub == 0)
+          for (int k = 1; k < nsub; ++k) {
+            a.x += sum[k * items + it].x;
+            a.y += sum[k * items + it].y;
+          }
+      }
+      if (sub == 0) *reinterpret_cast<float2 *>(&abar[h][2 * x]) = a;
+    }
+    __syncthreads();
+    // lane 4 r + h keeps row r of head h
+    static_assert(kMergeRows * kMergeHeads == 32, "a lane per result");
+    float mine = 0.f;
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-      if (k >= nh) break;
-      float a = red[k][0];
+    for (int r = 0; r < kMergeRows; ++r) {
+      float acc[kMergeHeads] = {};
 #pragma unroll
-      for (int i = 1; i < 8; ++i) a = fmaxf(a, red[k][i]);
-      // a's power of two; 1 for a head of zeros and for one that is not finite (its output is not either)
-      const int e = a > 0.f && a < INFINITY ? ilogbf(a) : 0;
-      const int64_t r = (int64_t)b * n_q + j * grp + h0 + k;
-      if (g < NA * kAtom)
-        reinterpret_cast<__half *>(qbuf)[r * (NA * kAtom) + ((g & ~7) | order_of<BITS>(g & 7))] =
-            __float2half_rn(scalbnf(v[k], -e));
-      if (tid == 0) sig[r] = scalbnf(1.f, e);
+      for (int i = 0; i < STEPS; ++i) {
+        const int g = 32 * VEC * i + VEC * lane;
+        if (g >= G) break;
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float lo = __uint_as_float(w[r][i][e / 2] << 16), hi = __uint_as_float(w[r][i][e / 2] & 0xFFFF0000u);
+#pragma unroll
+          for (int h = 0; h < kMergeHeads; ++h) {
+            const float2 a = *reinterpret_cast<const float2 *>(&abar[h][g + e]);
+            acc[h] = fmaf(lo, a.x, fmaf(hi, a.y, acc[h]));
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kMergeHeads; ++h) {
+        float v = acc[h];
+#pragma unroll
+        for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+        if (lane == 4 * r + h) mine = v;
+      }
+    }
+    if (lane % 4 < nh) {
+      const int64_t at = ((b * n_q + (int64_t)j * grp + h0 + lane % 4) * D) + warp * kMergeRows + lane / 4;
+      if (out_fp32) reinterpret_cast<float *>(o)[at] = mine;
+      else reinterpret_cast<uint16_t *>(o)[at] = f32_to_bf16_rn(mine);
     }
     __syncthreads();
   }
@@ -550,10 +640,10 @@ __global__ void __launch_bounds__(256) prefix_query(const uint16_t *__restrict__
 
 template <int BITS>
 cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float scale, const Params &p, uint8_t *qbuf,
-                     float *sig, MergeScratch ms, void *const *prof, cudaStream_t st) {
+                     float *sig, void *o, int out_fp32, void *const *prof, cudaStream_t st) {
   const Plan pl = plan_of(p.G, BITS);
-  cudaError_t e = launch_pdl(prefix_query<BITS>, dim3(n_kv, (unsigned)p.B), dim3(256), 0, st, q, W_kv, p.n_q, n_kv, p.G,
-                             pl.NA, scale * kLog2e, qbuf, sig, p.err, ms);
+  cudaError_t e = launch_pdl(prefix_query<BITS>, dim3(n_kv, (unsigned)p.B), dim3(kAbsorbThreads), 0, st, q, W_kv, p.n_q, n_kv,
+                             p.G, pl.NA, scale * kLog2e, qbuf, sig, p.err);
   if (e != cudaSuccess) return e;
   // one CTA per SM: each takes all of TMEM
   const size_t smem = pl.total > 120 * 1024 ? pl.total : 120 * 1024;
@@ -562,7 +652,11 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
   record_prof_event(prof[0], st);
   e = launch_pdl(prefix_split_tc<BITS>, dim3((unsigned)(p.QT * p.Sp + p.B * p.Ss)), dim3(kThreads), smem, st, p);
   record_prof_event(prof[1], st);
-  return e;
+  if (e != cudaSuccess) return e;
+  const int S = p.Sp + p.Ss;
+  auto merge = p.G % 4 == 0 ? prefix_merge<4> : prefix_merge<2>;
+  return launch_pdl(merge, dim3(n_kv, (unsigned)p.B), dim3(kMergeThreads), sizeof(float) * kMergeHeads * S, st,
+                    (const float *)p.part, S, p.n_q, n_kv, p.G, W_kv, o, out_fp32);
 }
 
 }  // namespace prefix
@@ -570,27 +664,22 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
 
 bool prefix_supported(int n_q, int G) { return n_q <= tc::prefix::kRows && G <= tc::prefix::kMaxG; }
 int prefix_rows_per_tile(int n_q) { return tc::prefix::kRows / n_q; }
+int prefix_max_splits() { return tc::prefix::kMaxSplits; }
 int prefix_tile_tokens() { return tc::prefix::kTile; }
 size_t prefix_query_bytes(int G) {  // Q' of one query head
   return (size_t)((G + tc::prefix::kAtom - 1) / tc::prefix::kAtom) * tc::prefix::kAtom * 2;
 }
 
-cudaError_t merge_absorbed_launch(const float *part, int S, int64_t B, int n_q, int n_kv, int d_h, int G,
-                                  const uint16_t *W_kv, void *o, int out_fp32, MergeScratch ms, cudaStream_t st,
-                                  int fold_bytes);
-
-cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, int d_h, const uint8_t *shared, int64_t Tp,
+cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, const uint8_t *shared, int64_t Tp,
                           const uint8_t *codes, int64_t bstride, int64_t T, const int32_t *seq_lens, int G, int bits,
                           const uint16_t *W_kv, float scale, int QT, int Sp, int Ss, int k, uint8_t *qbuf, float *sig,
-                          float *part, uint32_t *err, MergeScratch ms, void *o, int out_fp32, uint32_t stall_ns,
+                          float *part, uint32_t *err, void *o, int out_fp32, uint32_t stall_ns,
                           void *const *prof, cudaStream_t st) {
   tc::prefix::Params p{shared, codes, bstride, Tp, T, seq_lens, qbuf, sig, part, err,
                        (int)B, n_q, G, prefix_rows_per_tile(n_q), QT, Sp, Ss, k, stall_ns};
-  cudaError_t e = bits == 2   ? tc::prefix::launch_t<2>(q, W_kv, n_kv, scale, p, qbuf, sig, ms, prof, st)
-                  : bits == 4 ? tc::prefix::launch_t<4>(q, W_kv, n_kv, scale, p, qbuf, sig, ms, prof, st)
-                              : tc::prefix::launch_t<8>(q, W_kv, n_kv, scale, p, qbuf, sig, ms, prof, st);
-  if (e != cudaSuccess) return e;
-  return merge_absorbed_launch(part, Sp + Ss, B, n_q, n_kv, d_h, G, W_kv, o, out_fp32, ms, st, 0);
+  return bits == 2   ? tc::prefix::launch_t<2>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st)
+         : bits == 4 ? tc::prefix::launch_t<4>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st)
+                     : tc::prefix::launch_t<8>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st);
 }
 
 }  // namespace fsq

@@ -25,8 +25,8 @@
 // thread unpacks its token's row into Z in TMEM, the A operand (read from shared
 // memory, A would take twice its bandwidth); B is Q' in shared memory.
 //
-// Warps (16): 0 copies, 1 issues the MMAs, 4-7 and 8-11 take the scores of every
-// other 8 heads, 12-15 dequantise.  Every wait is bounded (FSQ_ERR_TIMEOUT).
+// Warps: 0 copies, 1 issues the MMAs, 4-7 and 8-11 take the scores of every other
+// 8 heads, 12-19 (12-15 with many heads) dequantise.  Every wait is bounded (FSQ_ERR_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -35,6 +35,7 @@
 
 #include "common.cuh"
 #include "f16_codes.cuh"
+#include "query_f16.cuh"
 #include "tc_decode.cuh"
 #include "tc_ptx.cuh"
 
@@ -43,13 +44,18 @@ namespace tc {
 namespace weights {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 512;
-constexpr int kDqWarps = 4;
+// Dequantising warps: eight, two per TMEM quarter, where a score thread keeps few
+// heads (640 threads have at most 96 registers each), else four.
+template <int NC>
+struct Shape {
+  static constexpr int DQ = NC <= 2 ? 8 : 4, THREADS = (12 + DQ) * 32;
+};
 constexpr int kAtom = 64;
 constexpr int kMaxQ = 64;             // query heads
 constexpr int kMaxStages = 8, kMaxZ = 4, kMaxS = 4;
 constexpr int kMiscBytes = 4096;
 constexpr size_t kSmemMax = 227 * 1024;
+constexpr int kTop = 12;              // Q' is scaled to a largest weight of 2^12 .. 2^13: its lo terms stay normal
 constexpr float kFar = 64.f;          // a score above the reference by more than 2^64 moves it
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 1000000000ull;
@@ -120,13 +126,12 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
 
-// One token's row [0, units) of 8-code groups at src -> Z columns.  LOAD(u)
-// gives 16 bytes of the row (piece u) or, in rows of other sizes, group u.
+// Pieces [first, pieces) of one token's row -> Z columns; load(u) gives the 16 bytes of piece u.
 template <int BITS, class F>
-__device__ __forceinline__ void fill_pieces(uint32_t z, int pieces, F load) {
+__device__ __forceinline__ void fill_pieces(uint32_t z, int first, int pieces, F load) {
   constexpr int PER = 128 / BITS / 2;  // columns of a piece: 8, 16, 32
 #pragma unroll 1
-  for (int u0 = 0; u0 < pieces; u0 += 4) {
+  for (int u0 = first; u0 < pieces; u0 += 4) {
     uint4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -159,12 +164,13 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
 
 // NC: 8-head chunks a score thread takes (of every other chunk)
 template <int BITS, int NC, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_constant__ CUtensorMap tmap, Params p) {
+__global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const __grid_constant__ CUtensorMap tmap, Params p) {
+  constexpr int kDqWarps = Shape<NC>::DQ;
   const Plan pl = plan_of(p.n_q, p.G, BITS);
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc &ms = *reinterpret_cast<Misc *>(smem + pl.off_misc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.G, Gp = pl.Gp, R = pl.R, N = pl.N, stages = pl.stages, nz = pl.nz, ns = pl.ns, n_q = p.n_q;
+  const int G = p.G, Gp = pl.Gp, NA = pl.NA, R = pl.R, N = pl.N, stages = pl.stages, nz = pl.nz, ns = pl.ns, n_q = p.n_q;
   const int split = blockIdx.x;
   const int64_t b = blockIdx.y;
   // the query prologue has waited for whatever wrote the codes and the lengths
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = ms.tmem_base;
+  constexpr uint32_t tm = 0;  // all 512 columns are this CTA's
   if (MODE == kLse) pdl_trigger();
   auto fail = [&]() {
     record_error(p.err, FSQ_ERR_TIMEOUT);
@@ -260,18 +266,20 @@ __global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_con
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
     const uint32_t id_s = idesc_f16(kTile, N, 0, 0);
-    const uint64_t b0 = desc_swz(smem_u32(smem), 16);
+    const uint32_t b0 = swz_lo(smem_u32(smem), 16), el = elect_one();
     Ring z, s;
     bool ok = warp_wait(&ms.q_full, 0, abort, kWaitNs);
     for (int i = 0; ok && i < n_tiles; ++i, z.next(nz), s.next(ns)) {
       ok = warp_wait(&ms.z_ready[z.slot], z.par, &ms.s_free[s.slot], s.par ^ 1u, abort, kWaitNs);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tm + pl.col_s + s.slot * N, a = tm + z.slot * (Gp / 2);
-#pragma unroll 4
-        for (int k = 0; k < Gp / 16; ++k)
-          mma_ts(d, a + 8 * k, b0 + (uint64_t)(((k >> 2) * N * 128 + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+      const uint32_t d = tm + pl.col_s + s.slot * N, a = tm + z.slot * (Gp / 2);
+#pragma unroll
+      for (int k = 0; k < (FSQ_MAX_G + 15) / 16; ++k) {  // atoms of 64 coordinates: four MMAs each
+        if (16 * k >= Gp) break;
+        mma_ts_warp(el, d, a + 8 * k, b0 + (k >> 2) * (N * 8) + 2 * (k & 3), id_s, k > 0 ? 1u : 0u);
+      }
+      if (el) {
         tc_commit(&ms.s_full[s.slot]);
         tc_commit(&ms.z_free[z.slot]);
       }
@@ -285,8 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_con
     // ------------------------------------------------------------ dequantisation: thread = token
     const int t = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    // a warp's share of the row's pieces or groups
+    constexpr int PARTS = kDqWarps / 4;
+    const int dq = (warp - 12) >> 2;
+    auto lo_of = [&](int n) { return (n + PARTS - 1) / PARTS * dq; };
+    auto hi_of = [&](int n) { return min(n, (n + PARTS - 1) / PARTS * (dq + 1)); };
     const int units = (G + 7) / 8, align = R % 4 == 0 ? 4 : R % 2 == 0 ? 2 : 1;
-    if (4 * units < Gp / 2)  // the group behind the last one stays zero
+    if (dq == 0 && 4 * units < Gp / 2)  // the group behind the last one stays zero
       for (int i = 0; i < nz; ++i) tmem_st4(tm + lanes + i * (Gp / 2) + 4 * units, make_uint4(0u, 0u, 0u, 0u));
     Ring c, z;
     for (int i = 0; i < n_tiles; ++i, c.next(stages), z.next(nz)) {
@@ -303,18 +316,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_con
       if (pl.tma) {
         if (rows == kTile) {
           const uint32_t o0 = (uint32_t)(t * R);
-          fill_pieces<BITS>(zt, R / 16, [&](int u) {
+          fill_pieces<BITS>(zt, lo_of(R / 16), hi_of(R / 16), [&](int u) {
             const uint32_t o = o0 + 16u * u;  // chunk (o / 16) % 8 of 128-byte row o / 128, swizzled
             return *reinterpret_cast<const uint4 *>(stage + (o ^ (((o >> 7) & 7u) << 4)));
           });
         } else {
-          fill_pieces<BITS>(zt, R / 16, [&](int u) { return *reinterpret_cast<const uint4 *>(row + 16 * u); });
+          fill_pieces<BITS>(zt, lo_of(R / 16), hi_of(R / 16), [&](int u) { return *reinterpret_cast<const uint4 *>(row + 16 * u); });
         }
       } else {
         const bool whole = rows == kTile;
         if (whole) row = stage + t * R;
 #pragma unroll 4
-        for (int u = 0; u < units; ++u) {
+        for (int u = lo_of(units); u < hi_of(units); ++u) {
           uint4 v;
           if (whole || u + 1 < units) {
             v = group8<BITS>(row, u, align);
@@ -490,92 +503,41 @@ __global__ void __launch_bounds__(kThreads, 1) weights_split_tc(const __grid_con
 // ---------------------------------------------------------------- prologue
 // Per (kv head j, batch row b): q'_h[g] = c sum_d W_k[j d_h + d][g] q_h[d] (c =
 // scale log2 e), scaled by the power of two that brings the head's largest
-// weight into [2^12, 2^13), as fp16 hi + lo in the score MMA's B layout: head h
+// weight into [2^kTop, 2^(kTop + 1)), as fp16 hi + lo in the score MMA's B layout: head h
 // is rows 16 (h / 8) + h % 8 (hi) and 8 further (lo) of 128-byte-swizzled atoms.
 // Also clears the error word.
 template <int BITS>
-__global__ void __launch_bounds__(256) weights_query(const uint16_t *__restrict__ q, const uint16_t *__restrict__ W_kv,
-                                                     int n_q, int n_kv, int G, int NA, int N, float c,
-                                                     uint8_t *__restrict__ qbuf, float *__restrict__ sig,
-                                                     uint32_t *err) {
-  constexpr int D = FSQ_HEAD_DIM, kHeads = 4, kMaxPer = (FSQ_MAX_G + 255) / 256;
-  __shared__ float qsm[kHeads][D];
-  __shared__ float red[kHeads][8];
-  const int j = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kAbsorbThreads, 1) weights_query(const uint16_t *__restrict__ q,
+                                                                const uint16_t *__restrict__ W_kv, int n_q, int n_kv,
+                                                                int G, int NA, int N, float c,
+                                                                uint8_t *__restrict__ qbuf, float *__restrict__ sig,
+                                                                uint32_t *err) {
+  __shared__ AbsorbSmem<FSQ_MAX_G> sm;
   const int64_t b = blockIdx.y;
-  const int grp = n_q / n_kv;
   pdl_wait();
   pdl_trigger();
-  if (j == 0 && b == 0 && tid == 0) *err = 0u;
+  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *err = 0u;
   uint8_t *dst = qbuf + b * ((int64_t)NA * N * 128);
+  auto at = [&](int n, int g) {  // row n, physical coordinate g
+    return dst + (g >> 6) * N * 128 + n * 128 + ((((g & 63) >> 3) ^ (n & 7)) << 4) + (g & 7) * 2;
+  };
   // heads that pad the last chunk of 8 are zero
-  if (j == 0)
-    for (int i = tid; i < (N / 2 - n_q) * NA * kAtom; i += 256) {
-      const int h = n_q + i / (NA * kAtom), g = i % (NA * kAtom);
-      for (int lo = 0; lo < 2; ++lo) {
-        const int n = (h >> 3) * 16 + lo * 8 + (h & 7);
-        *reinterpret_cast<uint16_t *>(dst + (g >> 6) * N * 128 + n * 128 + ((((g & 63) >> 3) ^ (n & 7)) << 4) +
-                                      (g & 7) * 2) = 0;
-      }
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < (N / 2 - n_q) * NA * kAtom; i += kAbsorbThreads) {
+      const int h = n_q + i / (NA * kAtom), n = (h >> 3) * 16 + (h & 7);
+      *reinterpret_cast<uint16_t *>(at(n, i % (NA * kAtom))) = 0;
+      *reinterpret_cast<uint16_t *>(at(n + 8, i % (NA * kAtom))) = 0;
     }
-  for (int h0 = 0; h0 < grp; h0 += kHeads) {
-    const int nh = min(kHeads, grp - h0);
-    for (int i = tid; i < kHeads * D; i += 256)
-      qsm[i / D][i % D] = i / D < nh ? bf16_to_f32(q[(b * n_q + j * grp + h0) * D + i]) : 0.f;
-    __syncthreads();
-    float v[kMaxPer][kHeads];
-    float top[kHeads] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < kMaxPer; ++x) {
-      const int g = tid + 256 * x;
-#pragma unroll
-      for (int k = 0; k < kHeads; ++k) v[x][k] = 0.f;
-      if (g < G) {
-        const uint16_t *w = W_kv + (int64_t)j * D * G + g;
-#pragma unroll 16
-        for (int d = 0; d < D; ++d) {
-          const float wd = bf16_to_f32(w[(int64_t)d * G]);
-#pragma unroll
-          for (int k = 0; k < kHeads; ++k) v[x][k] = fmaf(wd, qsm[k][d], v[x][k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-          v[x][k] *= c;
-          top[k] = fmaxf(top[k], fabsf(v[x][k]));
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-      if ((tid & 31) == 0) red[k][tid >> 5] = top[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-      if (k >= nh) break;
-      float a = red[k][0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) a = fmaxf(a, red[k][i]);
-      // 1 for a head of zeros and for one that is not finite (its weights are not either)
-      const int e = a > 0.f && a < INFINITY ? ilogbf(a) - 12 : 0;
-      const int h = j * grp + h0 + k, n = (h >> 3) * 16 + (h & 7);
-#pragma unroll
-      for (int x = 0; x < kMaxPer; ++x) {
-        const int g = tid + 256 * x;
-        if (g >= NA * kAtom) break;
-        const int ph = (g & ~7) | order_of<BITS>(g & 7);
-        const float s = scalbnf(v[x][k], -e);
+  absorb_heads(
+      sm, q, W_kv, n_q, n_kv, G, NA * kAtom, c, blockIdx.x, b,
+      [&](int h, int g, float v, int e) {
+        const int ph = (g & ~7) | order_of<BITS>(g & 7), n = (h >> 3) * 16 + (h & 7);
+        const float s = scalbnf(v, kTop - e);
         const __half hi = __float2half_rn(s);
-        uint8_t *at = dst + (ph >> 6) * N * 128 + n * 128 + ((((ph & 63) >> 3) ^ (n & 7)) << 4) + (ph & 7) * 2;
-        *reinterpret_cast<__half *>(at) = hi;
-        *reinterpret_cast<__half *>(at + 8 * 128) = __float2half_rn(s - __half2float(hi));
-      }
-      if (tid == 0) sig[b * n_q + h] = scalbnf(1.f, e);
-    }
-    __syncthreads();
-  }
+        *reinterpret_cast<__half *>(at(n, ph)) = hi;
+        *reinterpret_cast<__half *>(at(n + 8, ph)) = __float2half_rn(s - __half2float(hi));
+      },
+      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop); });
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -603,8 +565,8 @@ cudaError_t launch_nc(const CUtensorMap &map, const Params &p, int64_t B, const 
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.S, (unsigned)B);
   record_prof_event(prof[0], st);
-  e = launch_pdl(lse, grid, dim3(kThreads), smem, st, map, p);
-  if (e == cudaSuccess) e = launch_pdl(add, grid, dim3(kThreads), smem, st, map, p);
+  e = launch_pdl(lse, grid, dim3(Shape<NC>::THREADS), smem, st, map, p);
+  if (e == cudaSuccess) e = launch_pdl(add, grid, dim3(Shape<NC>::THREADS), smem, st, map, p);
   record_prof_event(prof[1], st);
   return e;
 }
@@ -630,7 +592,7 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_pdl(weights_query<BITS>, dim3(n_kv, (unsigned)B), dim3(256), 0, st, q, W_kv, p.n_q, n_kv, p.G,
+  cudaError_t e = launch_pdl(weights_query<BITS>, dim3(n_kv, (unsigned)B), dim3(kAbsorbThreads), 0, st, q, W_kv, p.n_q, n_kv, p.G,
                              pl.NA, pl.N, scale * kLog2e, qbuf, sig, p.err);
   if (e != cudaSuccess) return e;
   switch ((pl.N / 16 + 1) / 2) {

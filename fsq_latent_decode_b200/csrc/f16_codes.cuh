@@ -2,6 +2,8 @@
 // tensor-core kernels that dequantise to fp16 (shared-prefix attention,
 // attention weights).
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "tc_decode.cuh"
 #include "tc_ptx.cuh"
@@ -31,6 +33,47 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t par, volatile ui
 __device__ __forceinline__ bool warp_wait(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
                                           volatile uint32_t *abort, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, wait_bars(b0, p0, b1, p1, abort, limit_ns));
+}
+
+// The same, testing the phase for about a microsecond before the warp parks: for
+// the hand-offs of a tile, where the wake-up of a parked warp is what counts.
+__device__ __forceinline__ bool warp_spin(uint64_t *b, uint32_t par, volatile uint32_t *abort, uint64_t limit_ns) {
+  const uint32_t a = smem_u32(b);
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < 1 && !ok; ++i) ok = __all_sync(0xffffffffu, bar_test(a, par));
+  return ok || warp_wait(b, par, abort, limit_ns);
+}
+
+__device__ __forceinline__ bool warp_spin(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
+                                          volatile uint32_t *abort, uint64_t limit_ns) {
+  const uint32_t a0 = smem_u32(b0), a1 = smem_u32(b1);
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < 1 && !ok; ++i) ok = __all_sync(0xffffffffu, bar_test2(a0, p0, a1, p1));
+  return ok || warp_wait(b0, p0, b1, p1, abort, limit_ns);
+}
+
+// Waits for this thread's tcgen05.ld's; the registers they fill may not be used
+// before, also where other work stands between a load and its wait.
+#define FSQ_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : FSQ_RW8(r, 0), FSQ_RW8(r, 8)::"memory");
+}
+// More registers of loads that such a wait covers.
+__device__ __forceinline__ void tmem_held16(uint32_t *r) { asm volatile("" : FSQ_RW8(r, 0), FSQ_RW8(r, 8)); }
+
+// f(std::integral_constant<int, n>) for n in [LO, HI]: a loop whose step count the
+// compiler knows, for a count known at launch.
+template <int LO, int HI, class F>
+__device__ __forceinline__ void with_count(int n, F f) {
+  if constexpr (LO == HI) {
+    f(std::integral_constant<int, LO>());
+  } else {
+    constexpr int MID = (LO + HI) / 2;
+    if (n <= MID) with_count<LO, MID>(n, f);
+    else with_count<MID + 1, HI>(n, f);
+  }
 }
 
 // 128-byte-swizzled operand B of an MMA, as the two words of its descriptor.
@@ -92,11 +135,12 @@ __device__ __forceinline__ uint4 levels8(uint32_t w, uint32_t w2) {
   }
 }
 
-// Group u of a token (8 codes, BITS bytes) at `row` in shared memory, any alignment of the row
+// The BITS bytes of group u (8 codes) of the token at `row`, whose address and
+// whose neighbours' are multiples of `align`
 template <int BITS>
-__device__ __forceinline__ uint4 group8(const uint8_t *row, int u, int align) {
+__device__ __forceinline__ void group_words(const uint8_t *row, int u, int align, uint32_t (&w)[2]) {
   const uint8_t *p = row + u * BITS;
-  uint32_t w[2] = {0u, 0u};
+  w[0] = w[1] = 0u;
   if (align >= 4 && BITS >= 4) {
 #pragma unroll
     for (int i = 0; i < BITS / 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(p + 4 * i);
@@ -107,7 +151,6 @@ __device__ __forceinline__ uint4 group8(const uint8_t *row, int u, int align) {
 #pragma unroll
     for (int i = 0; i < BITS; ++i) w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
   }
-  return levels8<BITS>(w[0], w[1]);
 }
 
 }  // namespace tc

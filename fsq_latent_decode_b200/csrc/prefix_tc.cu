@@ -27,14 +27,21 @@
 //
 // Q' lives in TMEM as the A operand: read from shared memory, both operands of
 // a score MMA would need more than its bandwidth.  TMEM columns: O [0, Gp), Q'
-// (Gp / 2), then as many 64-column S buffers as fit, two at G = 256; P (fp16)
-// overlays the first half of its S.  Shared memory is a ring of dequantised
+// (Gp / 2), two P buffers of 32 (fp16), then as many 64-column S buffers as fit:
+// one at G = 256.  A softmax warp frees S as soon as it holds it in registers, so
+// the next scores run while this tile's exponentials do.  Shared memory is a ring of dequantised
 // tiles, deep enough that a tile waits in it from its scores to its pooling
 // while the next ones are made.
 //
-// Warps (16): 0 copies, 1 issues the MMAs, 4-7 and 8-11 the softmax of tokens
-// 0-31 and 32-63 of a tile (lane = query row), 12-15 dequantise.  The rescale
-// of a row's accumulator is decided by the two warps that hold its row.
+// Warps (16): 0 copies, 1 and 2 issue the MMAs, 4-7 and 8-11 take the softmax of
+// every other tile (lane = query row) and 12-13 and 14-15 its dequantisation: a
+// warp's way through a tile is a chain of waits and loads about twice as long as
+// the tensor core's, so two of them run side by side.  The two softmax warps of a
+// row agree on its reference tile by tile (`decided`).  Warps that take turns at
+// the tiles wait on barriers whose every phase is theirs (an even number of
+// stages and tile buffers; scores announced by the tile's parity): a barrier's
+// parity tells only neighbouring phases apart.  (For the same reason S has two
+// buffers at most: S(i + 2) is announced after S(i) has been read.)
 // Every wait is bounded (FSQ_ERR_TIMEOUT), as in the other decode kernels.
 #include "common.cuh"
 #include "f16_codes.cuh"
@@ -48,29 +55,27 @@ namespace prefix {
 
 constexpr int kRows = 128;                         // query rows of a tile
 constexpr int kTile = 64;                          // tokens of a tile
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;                      // 128 registers a thread: a softmax thread holds 64 scores
 constexpr int kAtom = 64;                          // coordinates of a swizzled atom row (128 bytes)
 constexpr int kAtomBytes = kTile * 128;            // 64 coordinates of a tile
-constexpr int kMaxG = 256;                         // O, Q' and two S buffers fill TMEM
-constexpr int kMaxStages = 6, kMaxZ = 6, kMaxS = 4;
-constexpr int kDqWarps = 4;
+constexpr int kMaxG = 256;                         // O, Q', two P and one S buffer fill TMEM
+constexpr int kMaxStages = 6, kMaxZ = 6, kMaxS = 2;
+constexpr int kDqWarps = 2;                        // of a group; the two groups take turns
 constexpr int kMiscBytes = 2048;
 constexpr size_t kSmemMax = 227 * 1024;
-// A row's reference m enters P as 2^kLift and moves when a score exceeds it by
-// 2^kTau, so P stays below 2^15 (fp16 ends at 2^16) and weights count down to
-// 2^-26 of the reference.  Random scores climb a few powers of two beyond a
-// tile's first maximum; moving O costs 1.5k cycles of a tile's 1.3k, so the
-// window is as wide as fp16 lets it be (kTau = 8: 97 us at G = 256, 131072
-// shared tokens, 16 rows; 13: see the table).
-constexpr float kTau = 13.f;
-constexpr float kLift = 2.f;
+// A row's reference m, its first tile's maximum, enters P as 2^0 and moves when a
+// score exceeds it by 2^kTau, so P stays below 2^15 (fp16 ends at 2^16) and
+// weights count down to 2^-24 of the reference.  Scores climb some powers of two
+// beyond a tile's first maximum, and moving O holds the whole CTA up for longer
+// than a tile takes, so the window is as wide as fp16 lets it be.
+constexpr float kTau = 15.f;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 1000000000ull;
 
 // Shared-memory and TMEM plan of a CTA.
 struct Plan {
   int Gp, NA, R, stages, nz, ns;
-  uint32_t z_bytes, stage_bytes, off_c, off_misc, total, col_q, col_s;
+  uint32_t z_bytes, stage_bytes, off_c, off_misc, total, col_q, col_p, col_s;
 };
 __host__ __device__ inline Plan plan_of(int G, int bits) {
   Plan p;
@@ -83,11 +88,12 @@ __host__ __device__ inline Plan plan_of(int G, int bits) {
   // +16: the last token's last group may read past its row
   p.stage_bytes = (uint32_t)(kTile * p.R + 16 + 127) / 128 * 128;
   p.stages = (int)((kSmemMax - kMiscBytes - p.off_c) / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
   p.off_misc = p.off_c + p.stages * p.stage_bytes;
   p.total = p.off_misc + kMiscBytes;
   p.col_q = p.Gp;
-  p.col_s = p.col_q + p.Gp / 2;
+  p.col_p = p.col_q + p.Gp / 2;
+  p.col_s = p.col_p + 2 * (kTile / 2);
   p.ns = (int)(512 - p.col_s) / kTile;
   if (p.ns > kMaxS) p.ns = kMaxS;
   return p;
@@ -110,10 +116,11 @@ struct Params {
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t z_ready[kMaxZ], z_free[kMaxZ];  // z_free: the tile's pooling is done
-  uint64_t s_full[kMaxS], p_ready[kMaxS];
-  uint64_t q_ready, done, never;
+  uint64_t s_full[2], s_free[kMaxS], p_ready[2];  // s_full, p_ready: even and odd tiles
+  uint64_t q_ready, done[2], never;
   uint32_t tmem_base, abort;
-  float mx[2][kRows];
+  uint64_t decided[2][4];                  // per softmax warp: the tile's reference stands
+  float m[kRows];                          // the rows' references
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
 
@@ -178,15 +185,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       mbar_init(&ms.z_free[i], 1);
     }
     for (int i = 0; i < kMaxS; ++i) {
-      mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.p_ready[i], 8);
+      mbar_init(&ms.s_free[i], 4);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_ready[i], 4);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(&ms.decided[i / 4][i % 4], 1);
     mbar_init(&ms.q_ready, 8);
-    mbar_init(&ms.done, 1);
+    mbar_init(&ms.done[0], 1);
+    mbar_init(&ms.done[1], 1);
     mbar_init(&ms.never, 1);  // completed by nothing: the test-only stall waits on it
     ms.abort = 0u;
     fence_mbar_init();
   }
+  if (tid < kRows) ms.m[tid] = -INFINITY;
   if (warp == 0) {
     tmem_alloc(&ms.tmem_base, 512);
     tmem_relinquish();
@@ -239,99 +252,122 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       for (int i = max(0, issued - stages); i < issued; ++i)
         drain_bar(&ms.full[i % stages], (uint32_t)(i / stages) & 1u, kDrainNs);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers (whole warps, one lane issues):
+    // one of the scores, one of the pooling.  Every wait costs a warp 100-200
+    // cycles even when its phase is complete; with two warps the tensor core has
+    // the other's MMAs meanwhile.  All hazards between them are barriers': S(i)
+    // overwrites scores that the softmax has loaded, P(i) follows S(i), and a
+    // tile is freed by its pooling.
     constexpr uint32_t id_s = idesc_f16(kRows, kTile, 0, 0);
     const uint32_t id_o = idesc_f16(kRows, Gp, 0, 1), el = elect_one();
-    Ring zs, zp, ss, sp, old;  // tile and S buffer of the next scores; of the next pooling; tile whose S is overwritten
-    auto scores = [&](int i) -> bool {
-      if (i >= ns) {  // this S buffer holds P(i - ns): its pooling must be done
-        if (!warp_wait(&ms.z_free[old.slot], old.par, abort, kWaitNs)) return false;
-        old.next(nz);
-      }
-      if (!warp_wait(&ms.z_ready[zs.slot], zs.par, abort, kWaitNs)) return false;
-      tc_fence_after();
-      const uint32_t d = tm + pl.col_s + ss.slot * kTile, a = tm + pl.col_q;
-      const uint32_t b = swz_lo(z_a + zs.slot * pl.z_bytes, 16);
+    bool ok = true;
+    if (warp == 1) {
+      ok = warp_wait(&ms.q_ready, 0, abort, kWaitNs);
+      with_count<1, kMaxG / 16>(Gp / 16, [&](auto ks) {
+      Ring z, s;
+      for (int i = 0; ok && i < n_tiles; ++i, z.next(nz), s.next(ns)) {
+        ok = warp_spin(&ms.s_free[s.slot], s.par ^ 1u, &ms.z_ready[z.slot], z.par, abort, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tm + pl.col_s + s.slot * kTile, a = tm + pl.col_q;
+        const uint32_t b = swz_lo(z_a + z.slot * pl.z_bytes, 16);
 #pragma unroll
-      for (int k = 0; k < kMaxG / 16; ++k) {
-        if (16 * k >= Gp) break;
-        mma_ts_warp(el, d, a + 8 * k, b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+        for (int k = 0; k < decltype(ks)::value; ++k)
+          mma_ts_warp(el, d, a + 8 * k, b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+        if (el) tc_commit(&ms.s_full[i & 1]);
+        __syncwarp();
       }
-      if (el) tc_commit(&ms.s_full[ss.slot]);
-      __syncwarp();
-      zs.next(nz);
-      ss.next(ns);
-      return true;
-    };
-    bool ok = warp_wait(&ms.q_ready, 0, abort, kWaitNs) && scores(0);
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      if (i + 1 < n_tiles) ok = scores(i + 1);
-      ok = ok && warp_wait(&ms.p_ready[sp.slot], sp.par, abort, kWaitNs);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t a = tm + pl.col_s + sp.slot * kTile;
-      const uint32_t b = swz_lo(z_a + zp.slot * pl.z_bytes, kAtomBytes);
+      });
+    } else {
+      Ring z, pr;
+      for (int i = 0; i < n_tiles; ++i, z.next(nz), pr.next(2)) {
+        ok = warp_spin(&ms.p_ready[pr.slot], pr.par, abort, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = tm + pl.col_p + pr.slot * (kTile / 2);
+        const uint32_t b = swz_lo(z_a + z.slot * pl.z_bytes, kAtomBytes);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts_warp(el, tm, a + 8 * k, b + ((k * 2048) >> 4), id_o, k > 0 || i > 0 ? 1u : 0u);
-      if (el) tc_commit(&ms.z_free[zp.slot]);
-      __syncwarp();
-      zp.next(nz);
-      sp.next(ns);
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts_warp(el, tm, a + 8 * k, b + ((k * 2048) >> 4), id_o, k > 0 || i > 0 ? 1u : 0u);
+        if (el) tc_commit(&ms.z_free[z.slot]);
+        __syncwarp();
+      }
     }
     if (!ok && lane == 0) fail();
     // every issued MMA finishes before TMEM is freed
-    tc_commit_elect(&ms.done);
-    mbar_wait_fixed(&ms.done, 0, kDrainNs);
+    tc_commit_elect(&ms.done[warp - 1]);
+    mbar_wait_fixed(&ms.done[warp - 1], 0, kDrainNs);
   } else if (warp >= 12) {
     // ------------------------------------------------------------ dequantisation
-    const int dt = tid - 12 * 32;
+    const int grp = (warp - 12) / kDqWarps, dt = tid - (12 + kDqWarps * grp) * 32;
     const int align = R % 16 == 0 ? 16 : R % 4 == 0 ? 4 : R % 2 == 0 ? 2 : 1;
     const int units = (G + 7) / 8;   // groups of 8 coordinates that hold codes
     // the groups behind them stay zero
-    for (int i = dt; i < kTile * (8 * NA - units) * nz; i += kDqWarps * 32) {
+    static_assert(kMaxZ % 2 == 0 && kMaxStages % 2 == 0, "a group always takes the same stages and tile buffers");
+    for (int i = dt; i < kTile * (8 * NA - units) * (nz / 2); i += kDqWarps * 32) {
       const int t = i % kTile, x = i / kTile;
-      *reinterpret_cast<uint4 *>(smem + (x % nz) * pl.z_bytes + z_at(t, units + x / nz)) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4 *>(smem + (2 * (x % (nz / 2)) + grp) * pl.z_bytes + z_at(t, units + x / (nz / 2))) =
+          make_uint4(0u, 0u, 0u, 0u);
     }
     Ring cr, zr;
     for (int i = 0; i < n_tiles; ++i, cr.next(stages), zr.next(nz)) {
-      if (!warp_wait(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
+      if ((i & 1) != grp) continue;
+      if (!warp_spin(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
         if (lane == 0) fail();
         break;
       }
       const uint8_t *c = smem + pl.off_c + cr.slot * pl.stage_bytes;
       uint8_t *z = smem + zr.slot * pl.z_bytes;
       if (align == 16) {
-        // 16 bytes of a row at a time, in order: the reads are contiguous over
-        // the warp and the swizzle spreads the writes over the banks
+        // 16 bytes of a row at a time, in order, so that the reads are contiguous
+        // over the warp.  Eight lanes then hold neighbouring pieces of one token,
+        // whose chunks of the same rank share banks: each lane starts at another
+        // of its NE chunks, and the eight writes of a step cover all banks.
+        constexpr int NE = 16 / BITS;                  // chunks (groups of 8 coordinates) of a piece
         const int ppr = R / 16;
         const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 64 * 16
 #pragma unroll 4
         for (int x = dt; x < kTile * ppr; x += kDqWarps * 32) {
           const int t = (int)(((uint32_t)x * inv) >> 16), piece = x - t * ppr;
           const uint4 v = *reinterpret_cast<const uint4 *>(c + 16 * x);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          if constexpr (BITS == 8) {
+          const int rot = (piece * NE >> 3) & (NE - 1);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};        // rotated right by rot groups
+          {
+            const int by = rot * BITS / 4;             // whole words
+            if (by & 1) {
+              const uint32_t f = w[0];
+              w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = f;
+            }
+            if (by & 2) {
+              const uint32_t f = w[0], g = w[1];
+              w[0] = w[2], w[1] = w[3], w[2] = f, w[3] = g;
+            }
+            if constexpr (BITS == 2) {                 // and half of one
+              const uint32_t sh = 16u * (rot & 1), f = w[0];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              *reinterpret_cast<uint4 *>(z + z_at(t, 2 * piece + e)) = levels8<8>(w[2 * e], w[2 * e + 1]);
-          } else if constexpr (BITS == 4) {
+              for (int e = 0; e < 3; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], sh);
+              w[3] = __funnelshift_r(w[3], f, sh);
+            }
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(z + z_at(t, 4 * piece + e)) = levels8<4>(w[e], 0u);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4 *>(z + z_at(t, 8 * piece + e)) = levels8<2>(w[e / 2] >> (16 * (e & 1)), 0u);
+          for (int e = 0; e < NE; ++e) {
+            uint4 l;
+            if constexpr (BITS == 8) l = levels8<8>(w[2 * e], w[2 * e + 1]);
+            else if constexpr (BITS == 4) l = levels8<4>(w[e], 0u);
+            else l = levels8<2>(w[e / 2] >> (16 * (e & 1)), 0u);
+            *reinterpret_cast<uint4 *>(z + z_at(t, NE * piece + ((e + rot) & (NE - 1)))) = l;
           }
         }
       } else {
-        // a token's even or odd groups per thread
-        const int t = dt % kTile;
-        const uint8_t *rowp = c + t * R;
+        // a group at a time; the lanes hold neighbouring tokens
 #pragma unroll 4
-        for (int u = dt / kTile; u < units; u += kDqWarps * 32 / kTile)
-          *reinterpret_cast<uint4 *>(z + z_at(t, u)) = group8<BITS>(rowp, u, align);
+        for (int x = dt; x < kTile * units; x += kDqWarps * 32) {
+          const int t = x % kTile, u = x / kTile;
+          uint32_t w[2];
+          group_words<BITS>(c + t * R, u, align, w);
+          *reinterpret_cast<uint4 *>(z + z_at(t, u)) = levels8<BITS>(w[0], w[1]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -341,13 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       }
     }
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax: lane = query row, 32 tokens
+    // ------------------------------------------------------------ softmax: lane = query row, every other tile
     const int wg = (warp - 4) >> 2, q4 = warp & 3;
     const int r = 32 * q4 + lane;
     const bool busy = 32 * q4 < r_hi && 32 * q4 + 32 > r_lo;  // this warp has live rows
     const bool live = r >= r_lo && r < r_hi;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-    const int pair = 1 + q4;  // barrier of the two warps of these rows
     bool ok = true;
     pdl_wait();  // Q' and sig come from the query prologue
     float sig = 0.f;
@@ -372,82 +407,103 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     }
     // test-only stall: a wait that runs out on purpose (nothing completes `never`)
     if (p.stall_ns != 0u && !warp_wait(&ms.never, 0, abort, p.stall_ns)) ok = false;
-    float m = -INFINITY, l = 0.f;
-    Ring sr, zo;  // S buffer of the tile; tile before it
-    for (int i = 0; i < n_tiles; ++i, sr.next(ns)) {
-      ok = ok && warp_wait(&ms.s_full[sr.slot], sr.par, abort, kWaitNs);
+    float m = -INFINITY, l = 0.f;  // the reference that l is relative to, which the other warp may have moved since
+    Ring sr, zo, zp;               // S buffer of the tile; the tile before it; the one before that
+    if (wg == 1) sr.next(ns), zp.next(nz);
+    else zo.next(nz);
+    for (int i = wg; ok && i < n_tiles; i += 2) {
+      ok = warp_spin(&ms.s_full[wg], (uint32_t)(i >> 1) & 1u, abort, kWaitNs);
       tc_fence_after();
-      uint32_t s[32];
+      uint32_t s[64];
       float top = -INFINITY;
-      const uint32_t ts = tm + lanes + pl.col_s + sr.slot * kTile;
       if (busy) {
-        tmem_ld32(ts + 32 * wg, s);
-        tmem_ld_wait();
-        const int valid = (int)min((int64_t)kTile, t1 - (t0 + (int64_t)i * kTile)) - 32 * wg;  // tokens of this half
-        if (valid < 32) {
+        const uint32_t ts = tm + lanes + pl.col_s + sr.slot * kTile;
+        tmem_ld32(ts, s);
+        tmem_ld32(ts + 32, s + 32);
+        tmem_ld_wait16(s);
+        tmem_held16(s + 16);
+        tmem_held16(s + 32);
+        tmem_held16(s + 48);
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.s_free[sr.slot]);
+      sr.next(ns);
+      sr.next(ns);
+      if (busy) {
+        const int valid = (int)min((int64_t)kTile, t1 - (t0 + (int64_t)i * kTile));
+        if (valid < kTile) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
+          for (int c = 0; c < kTile; ++c)
             if (c >= valid) s[c] = 0xFF800000u;  // -inf
         }
         float t2[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 32; c += 8)
+        for (int c = 0; c < kTile; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             t2[e] = fmax3f(t2[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
         top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3])) * sig;
-        if (!live) top = -INFINITY;
       }
-      // both warps have read S before P overwrites it; they decide together
-      if (named_bar_or(pair, 64, !ok || top > m + kTau || (i == 0 && live))) {
-        ms.mx[wg][r] = top;
-        if (named_bar_or(pair, 64, !ok)) {
-          ok = false;
-          break;
+      // the row's reference after the tile before this one, which the other warp has decided
+      if (i > 0) ok = warp_spin(&ms.decided[wg ^ 1][q4], (uint32_t)((i - 1) >> 1) & 1u, abort, kWaitNs) && ok;
+      const float was = *(volatile float *)&ms.m[r];
+      const bool raise = live && (top > was + kTau || (i == 0 && top > was));
+      const float now = raise ? top : was;
+      if (raise) *(volatile float *)&ms.m[r] = now;
+      const bool move = __any_sync(0xffffffffu, raise) && i > 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.decided[wg][q4]);
+      if (m != now) l *= exp2f(m - now);
+      m = now;
+      // P(i - 2) has been pooled (a warp without live rows waits too: its arrival
+      // for this tile must not count for that one)
+      if (i > 1) ok = warp_spin(&ms.z_free[zp.slot], zp.par, abort, kWaitNs) && ok;
+      tc_fence_after();
+      if (busy) {
+        const uint32_t tp = tm + lanes + pl.col_p + wg * (kTile / 2);
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < kTile / 2; c0 += 8) {
+          uint32_t h[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * (c0 + c)]), sig, -now));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * (c0 + c) + 1]), sig, -now));
+            l4[(2 * c) & 3] += e0;
+            l4[(2 * c + 1) & 3] += e1;
+            const __half2 v = __floats2half2_rn(e0, e1);
+            h[c] = *reinterpret_cast<const uint32_t *>(&v);
+          }
+          tmem_st8(tp + c0, h);
         }
-        const float mn = fmaxf(m, fmaxf(ms.mx[0][r], ms.mx[1][r]));
-        const float f = mn == m ? 1.f : exp2f(m - mn);
-        l *= f;
-        m = mn;
-        if (i > 0 && busy) {
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if (move) {
           // O holds every earlier tile once the last pooling is done
-          if (!warp_wait(&ms.z_free[zo.slot], zo.par, abort, kWaitNs)) ok = false;
+          const float f = raise ? exp2f(was - now) : 1.f;
+          ok = warp_spin(&ms.z_free[zo.slot], zo.par, abort, kWaitNs) && ok;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 16 * wg; c < Gp; c += 64) {  // the warps take turns at 16 columns, two turns at once
+          for (int c = 0; c < Gp; c += 32) {
             uint32_t a[32];
-            const bool two = c + 32 < Gp;
+            const bool two = c + 16 < Gp;
             tmem_ld16(tm + lanes + c, a);
-            if (two) tmem_ld16(tm + lanes + c + 32, a + 16);
-            tmem_ld_wait();
+            if (two) tmem_ld16(tm + lanes + c + 16, a + 16);
+            tmem_ld_wait16(a);
+            tmem_held16(a + 16);
 #pragma unroll
             for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
             tmem_st16(tm + lanes + c, a);
-            if (two) tmem_st16(tm + lanes + c + 32, a + 16);
+            if (two) tmem_st16(tm + lanes + c + 16, a + 16);
           }
         }
-      }
-      if (busy) {
-        const float off = kLift - m;
-        uint32_t h[16];
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * c]), sig, off));
-          const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * c + 1]), sig, off));
-          l4[(2 * c) & 3] += e0;
-          l4[(2 * c + 1) & 3] += e1;
-          const __half2 v = __floats2half2_rn(e0, e1);
-          h[c] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        tmem_st16(ts + 16 * wg, h);
         tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.p_ready[sr.slot]);
-      if (i > 0) zo.next(nz);
+      if (lane == 0) mbar_arrive(&ms.p_ready[wg]);
+      if (i > 0) zo.next(nz), zo.next(nz);
+      if (i > 1) zp.next(nz), zp.next(nz);
     }
     // ---- epilogue: O through shared memory (the tiles are spent) to the partials
     if (ok) {
@@ -455,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       ok = warp_wait(&ms.z_free[z], (uint32_t)((n_tiles - 1) / nz) & 1u, abort, kWaitNs);
     }
     if (!ok) fail();
-    ms.mx[wg][r] = l;
+    // behind the staged O, which the Z tiles leave room for: per group (reference, sum) of a row
+    float2 *sums = reinterpret_cast<float2 *>(smem + pl.off_c) - 2 * kRows;
+    sums[wg * kRows + r] = make_float2(m, l);
     if (!named_bar_or(5, 256, !ok)) {
       tc_fence_after();
       float *stage = reinterpret_cast<float *>(smem);  // [128][Gp + 1]: conflict-free both ways
@@ -465,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
         for (int c = 16 * wg; c < Gp; c += 32) {
           uint32_t a[16];
           tmem_ld16(tm + lanes + c, a);
-          tmem_ld_wait();
+          tmem_ld_wait16(a);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int g = c + (e & 8) + (BITS == 8 ? (e & 7) : ((e & 1) << 2) + ((e & 7) >> 1));
@@ -475,13 +533,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       }
       named_bar(5, 256);
       for (int rr = r_lo + (warp - 4); rr < r_hi; rr += 8) {
-        float *out = record(rr);
-        for (int g = lane; g < G; g += 32) out[2 + g] = stage[rr * ld + g];
+        float *out = record(rr) + 2;
+        const float *from = stage + rr * ld;
+        float v[kMaxG / 32];
+#pragma unroll
+        for (int x = 0; x < kMaxG / 32; ++x) v[x] = 32 * x + lane < G ? from[32 * x + lane] : 0.f;
+#pragma unroll
+        for (int x = 0; x < kMaxG / 32; ++x)
+          if (32 * x + lane < G) out[32 * x + lane] = v[x];
       }
       if (live && wg == 0) {
         float *out = record(r);
-        out[0] = m - kLift;
-        out[1] = ms.mx[0][r] + ms.mx[1][r];
+        const float2 a = sums[r], c = sums[kRows + r];
+        const float last = ms.m[r];
+        out[0] = last;
+        out[1] = a.y * exp2f(a.x - last) + (n_tiles > 1 ? c.y * exp2f(c.x - last) : 0.f);
       }
     }
   }
@@ -520,119 +586,156 @@ __global__ void __launch_bounds__(kAbsorbThreads, 1) prefix_query(const uint16_t
 // ---------------------------------------------------------------- split merge
 // Per (kv head j, batch row b): the group's heads, four at a time,
 //   m = max_s m_s,  w_s = 2^(m_s - m),  abar_h = sum_s w_s O_s / sum_s w_s l_s,  o_h = W_v^(j) abar_h.
-// A thread sums one coordinate pair of one head over its share of the splits
-// (the loads of eight splits are in flight together); a warp then takes eight
-// rows of W_v, loaded into registers before the wait for the split kernel.
+// Bound by latency (35 splits of 4 heads at G = 256: 140 KB of partials and 64 KB
+// of W_v per CTA).  W_v^(j) comes into shared memory before the wait for the
+// split kernel; a thread sums one coordinate pair of one head over its share of
+// the splits, the first eight of them loaded while a warp per head forms w_s; a
+// warp then takes eight rows of W_v, the heads' sums in registers, and one
+// butterfly folds the 32 results over its lanes.
 constexpr int kMergeThreads = 512, kMergeHeads = 4, kMergeRows = FSQ_HEAD_DIM / (kMergeThreads / 32);
+constexpr int kMergeAhead = 8;
 constexpr int kMaxSplits = 2048;  // of a row
 
-// VEC: coordinates a lane reads of a W_v row at once (4, or 2 where G is not a multiple of 4)
+// VEC: coordinates that are moved at once (8, or 2 where G is not a multiple of 8)
 template <int VEC>
 __global__ void __launch_bounds__(kMergeThreads, 1) prefix_merge(const float *__restrict__ part, int S, int n_q, int n_kv,
-                                                              int G, const uint16_t *__restrict__ W_kv, void *o,
-                                                              int out_fp32) {
+                                                                 int G, const uint16_t *__restrict__ W_kv, void *o,
+                                                                 int out_fp32) {
   constexpr int D = FSQ_HEAD_DIM, STEPS = kMaxG / (32 * VEC);
-  extern __shared__ __align__(16) float wts[];  // [kMergeHeads][S]: w_s / sum
+  extern __shared__ __align__(16) uint8_t msm[];
+  uint16_t *wv = reinterpret_cast<uint16_t *>(msm);                                // [D][G]
+  float2 *wts = reinterpret_cast<float2 *>(msm + sizeof(uint16_t) * D * G);        // [kMergeHeads][S]: (m, l), then w in x
   __shared__ float2 sum[kMergeThreads];
   __shared__ __align__(16) float abar[kMergeHeads][kMaxG];
   const int j = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t b = blockIdx.y;
   const int grp = n_q / n_kv;
-  // rows kMergeRows * warp .. of W_v^(j); coordinates 32 VEC i + VEC lane ..
-  uint32_t w[kMergeRows][STEPS][VEC / 2];
-#pragma unroll
-  for (int r = 0; r < kMergeRows; ++r)
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int g = 32 * VEC * i + VEC * lane;
-      const uint16_t *src = W_kv + ((int64_t)(n_kv + j) * D + warp * kMergeRows + r) * G + g;
-      if constexpr (VEC == 4) {
-        const uint2 v = g < G ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
-        w[r][i][0] = v.x, w[r][i][1] = v.y;
-      } else {
-        w[r][i][0] = g < G ? *reinterpret_cast<const uint32_t *>(src) : 0u;
-      }
+  {
+    const uint16_t *src = W_kv + (int64_t)(n_kv + j) * D * G;
+    for (int i = tid; i < D * G / VEC; i += kMergeThreads) {
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(wv + i * VEC);
+      if constexpr (VEC == 8) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src + i * VEC) : "memory");
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(src + i * VEC) : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   pdl_wait();
   const int64_t hs = 2 + G, ss = (int64_t)n_q * hs;  // floats of a record, of a split
   for (int h0 = 0; h0 < grp; h0 += kMergeHeads) {
     const int nh = min(kMergeHeads, grp - h0);
     const float *rec = part + (b * S * n_q + (int64_t)j * grp + h0) * hs;
+    const int pairs = G / 2, items = nh * pairs, nsub = min(16, max(1, kMergeThreads / items));  // items <= 4 * 128
+    const int it = tid % items, sub = tid / items, h = it / pairs, x = it % pairs;
+    const float *src = rec + h * hs + 2 + 2 * x;
+    float2 first[kMergeAhead];
+#pragma unroll
+    for (int k = 0; k < kMergeAhead; ++k) {
+      const int s = sub + k * nsub;
+      first[k] = sub < nsub && s < S ? *reinterpret_cast<const float2 *>(src + s * ss) : make_float2(0.f, 0.f);
+    }
     if (warp < nh) {  // a warp per head: the splits' weights
       float m = -INFINITY, l = 0.f;
-      for (int s = lane; s < S; s += 32) m = fmaxf(m, rec[s * ss + warp * hs]);
+      for (int s = lane; s < S; s += 32) {
+        const float2 v = *reinterpret_cast<const float2 *>(rec + s * ss + warp * hs);
+        wts[warp * S + s] = v;
+        m = fmaxf(m, v.x);
+      }
 #pragma unroll
       for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
       for (int s = lane; s < S; s += 32) {
-        const float2 ml = *reinterpret_cast<const float2 *>(rec + s * ss + warp * hs);
-        const float e = exp2f(ml.x - m);  // 0 for an empty split
-        wts[warp * S + s] = e;
-        l = fmaf(e, ml.y, l);
+        const float2 v = wts[warp * S + s];
+        const float e = exp2f(v.x - m);  // 0 for an empty split
+        wts[warp * S + s].x = e;
+        l = fmaf(e, v.y, l);
       }
 #pragma unroll
       for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
       const float inv = 1.f / l;
-      for (int s = lane; s < S; s += 32) wts[warp * S + s] *= inv;
+      for (int s = lane; s < S; s += 32) wts[warp * S + s].x *= inv;
     }
     __syncthreads();
-    const int pairs = G / 2, items = nh * pairs, nsub = min(16, max(1, kMergeThreads / items));
-    {
-      const int it = tid % items, sub = tid / items, h = it / pairs, x = it % pairs;  // items <= 4 * 128
-      float2 a = make_float2(0.f, 0.f);
-      if (sub < nsub) {
-        const float *src = rec + h * hs + 2 + 2 * x;
+    float2 a = make_float2(0.f, 0.f);
+    if (sub < nsub) {
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const int s = sub + k * nsub;
+        const float e = s < S ? wts[h * S + s].x : 0.f;
+        a.x = fmaf(e, first[k].x, a.x);
+        a.y = fmaf(e, first[k].y, a.y);
+      }
 #pragma unroll 8
-        for (int s = sub; s < S; s += nsub) {
-          const float2 v = *reinterpret_cast<const float2 *>(src + s * ss);
-          const float e = wts[h * S + s];
-          a.x = fmaf(e, v.x, a.x);
-          a.y = fmaf(e, v.y, a.y);
-        }
+      for (int s = sub + kMergeAhead * nsub; s < S; s += nsub) {
+        const float2 v = *reinterpret_cast<const float2 *>(src + s * ss);
+        const float e = wts[h * S + s].x;
+        a.x = fmaf(e, v.x, a.x);
+        a.y = fmaf(e, v.y, a.y);
       }
-      if (nsub > 1) {
-        sum[tid] = a;
-        __syncthreads();
-        if (sub == 0)
-          for (int k = 1; k < nsub; ++k) {
-            a.x += sum[k * items + it].x;
-            a.y += sum[k * items + it].y;
-          }
-      }
-      if (sub == 0) *reinterpret_cast<float2 *>(&abar[h][2 * x]) = a;
     }
+    if (nsub > 1) {
+      sum[tid] = a;
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < nsub; ++k) {
+          a.x += sum[k * items + it].x;
+          a.y += sum[k * items + it].y;
+        }
+    }
+    if (sub == 0) *reinterpret_cast<float2 *>(&abar[h][2 * x]) = a;
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    // lane 4 r + h keeps row r of head h
+    float av[kMergeHeads][STEPS][VEC];
+#pragma unroll
+    for (int k = 0; k < kMergeHeads; ++k)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int g = 32 * VEC * i + VEC * lane + e;
+          av[k][i][e] = k < nh && g < G ? abar[k][g] : 0.f;
+        }
+    // 32 results a warp: row warp * kMergeRows + r of head k at 4 r + k
     static_assert(kMergeRows * kMergeHeads == 32, "a lane per result");
-    float mine = 0.f;
+    float acc[32];
 #pragma unroll
     for (int r = 0; r < kMergeRows; ++r) {
-      float acc[kMergeHeads] = {};
+#pragma unroll
+      for (int k = 0; k < kMergeHeads; ++k) acc[4 * r + k] = 0.f;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int g = 32 * VEC * i + VEC * lane;
-        if (g >= G) break;
-#pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          const float lo = __uint_as_float(w[r][i][e / 2] << 16), hi = __uint_as_float(w[r][i][e / 2] & 0xFFFF0000u);
-#pragma unroll
-          for (int h = 0; h < kMergeHeads; ++h) {
-            const float2 a = *reinterpret_cast<const float2 *>(&abar[h][g + e]);
-            acc[h] = fmaf(lo, a.x, fmaf(hi, a.y, acc[h]));
+        uint32_t w[VEC / 2] = {};
+        if (g < G) {
+          const uint16_t *row = wv + (warp * kMergeRows + r) * G + g;
+          if constexpr (VEC == 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(row);
           }
         }
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2)
+#pragma unroll
+          for (int k = 0; k < kMergeHeads; ++k) {
+            acc[4 * r + k] = fmaf(__uint_as_float(w[e / 2] << 16), av[k][i][e], acc[4 * r + k]);
+            acc[4 * r + k] = fmaf(__uint_as_float(w[e / 2] & 0xFFFF0000u), av[k][i][e + 1], acc[4 * r + k]);
+          }
       }
+    }
+    // butterfly: every step hands the other half of the results over; lane x ends with result x
 #pragma unroll
-      for (int h = 0; h < kMergeHeads; ++h) {
-        float v = acc[h];
+    for (int k = 16; k; k >>= 1) {
+      const bool up = lane & k;
 #pragma unroll
-        for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-        if (lane == 4 * r + h) mine = v;
+      for (int i = 0; i < k; ++i) {
+        const float give = up ? acc[i] : acc[i + k], keep = up ? acc[i + k] : acc[i];
+        acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, k);
       }
     }
     if (lane % 4 < nh) {
       const int64_t at = ((b * n_q + (int64_t)j * grp + h0 + lane % 4) * D) + warp * kMergeRows + lane / 4;
-      if (out_fp32) reinterpret_cast<float *>(o)[at] = mine;
-      else reinterpret_cast<uint16_t *>(o)[at] = f32_to_bf16_rn(mine);
+      if (out_fp32) reinterpret_cast<float *>(o)[at] = acc[0];
+      else reinterpret_cast<uint16_t *>(o)[at] = f32_to_bf16_rn(acc[0]);
     }
     __syncthreads();
   }
@@ -654,9 +757,12 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
   record_prof_event(prof[1], st);
   if (e != cudaSuccess) return e;
   const int S = p.Sp + p.Ss;
-  auto merge = p.G % 4 == 0 ? prefix_merge<4> : prefix_merge<2>;
-  return launch_pdl(merge, dim3(n_kv, (unsigned)p.B), dim3(kMergeThreads), sizeof(float) * kMergeHeads * S, st,
-                    (const float *)p.part, S, p.n_q, n_kv, p.G, W_kv, o, out_fp32);
+  auto merge = p.G % 8 == 0 ? prefix_merge<8> : prefix_merge<2>;
+  const size_t msm = sizeof(uint16_t) * FSQ_HEAD_DIM * p.G + sizeof(float2) * kMergeHeads * S;
+  e = ensure_smem_limit((const void *)merge, msm);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(merge, dim3(n_kv, (unsigned)p.B), dim3(kMergeThreads), msm, st, (const float *)p.part, S, p.n_q,
+                    n_kv, p.G, W_kv, o, out_fp32);
 }
 
 }  // namespace prefix

@@ -11,7 +11,11 @@
 //
 // The result is a running fp32 sum over many steps, so scores are exact to fp32:
 // Q' = W_k^T q * scale * log2 e is held as two fp16 terms per head (22 bits),
-// scaled by a power of two, against exact fp16 levels.
+// scaled by a power of two, against the codes n themselves: the level offset
+// -L/2 moves all of a head's scores alike, which the softmax does not see.  A
+// code stays where it lies in its word, as the mantissa of an fp16 subnormal
+// (n 2^-24 times the power of two of its place, which Q' takes off): one LOP3 per
+// pair.
 //   S [128 tokens x 2 n_q] = Z [128 x G] . [Q'_hi ; Q'_lo]^T      score = S_hi + S_lo
 // A token is a TMEM lane, so a softmax thread owns its tokens: kLse keeps
 // (reference, sum) per head and thread, the first token's score as the
@@ -25,8 +29,10 @@
 // thread unpacks its token's row into Z in TMEM, the A operand (read from shared
 // memory, A would take twice its bandwidth); B is Q' in shared memory.
 //
-// Warps: 0 copies, 1 issues the MMAs, 4-7 and 8-11 take the scores of every other
-// 8 heads, 12-19 (12-15 with many heads) dequantise.  Every wait is bounded (FSQ_ERR_TIMEOUT).
+// Warps: 0 copies, 1 and 2 issue the MMAs of every other tile, 4-7 and 8-11 take
+// the scores, 12-19 (12-15 with many heads) dequantise.  A warp's way through a
+// tile is a chain of waits and loads, so two of each kind run side by side.
+// Every wait is bounded (FSQ_ERR_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -44,11 +50,12 @@ namespace tc {
 namespace weights {
 
 constexpr int kTile = 128;
-// Dequantising warps: eight, two per TMEM quarter, where a score thread keeps few
-// heads (640 threads have at most 96 registers each), else four.
+// Dequantising warps: two per TMEM quarter, which halve a token's row, where a
+// score thread keeps few heads (640 threads have at most 96 registers each), else
+// one.
 template <int NC>
 struct Shape {
-  static constexpr int DQ = NC <= 2 ? 8 : 4, THREADS = (12 + DQ) * 32;
+  static constexpr int PARTS = NC <= 2 ? 2 : 1, DQ = 4 * PARTS, THREADS = (12 + DQ) * 32;
 };
 constexpr int kAtom = 64;
 constexpr int kMaxQ = 64;             // query heads
@@ -61,9 +68,29 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 1000000000ull;
 enum Mode { kLse, kAdd };
 
+// n buffers that tiles take in turn.  Warps that take every other tile wait on
+// barriers whose every phase is theirs (a barrier's parity tells only
+// neighbouring phases apart): n is a power of two, and one buffer has two barriers,
+// for even and odd tiles.
+struct Slots {
+  int n, nb, lb;  // buffers, barriers (a power of two: 2^lb)
+  __host__ __device__ explicit Slots(int fit = 1, int most = 1) {
+    n = 1;
+    while (2 * n <= fit && 2 * n <= most) n *= 2;
+    nb = n < 2 ? 2 : n;
+    for (lb = 1; (1 << lb) < nb; ++lb) {
+    }
+  }
+  __device__ __forceinline__ int buf(int i) const { return i & (n - 1); }
+  __device__ __forceinline__ int bar(int i) const { return i & (nb - 1); }
+  __device__ __forceinline__ uint32_t par(int i) const { return (uint32_t)(i >> lb) & 1u; }
+};
+
 struct Plan {
-  int Gp, NA, R, N, stages, nz, ns;  // N: score columns (16 per 8 heads)
+  int Gp, NA, R, N;   // N: score columns, 16 (hi, lo) per 8 heads, 32 NC in all
+  Slots st, z, s;    // code stages in shared memory; Z and S buffers in TMEM
   bool tma;
+  bool fits;
   uint32_t q_bytes, stage_bytes, off_misc, total, col_s;
 };
 __host__ __device__ inline Plan plan_of(int n_q, int G, int bits) {
@@ -71,22 +98,21 @@ __host__ __device__ inline Plan plan_of(int n_q, int G, int bits) {
   p.Gp = (G + 15) / 16 * 16;
   p.NA = (G + kAtom - 1) / kAtom;
   p.R = G * bits / 8;
-  p.N = (n_q + 7) / 8 * 16;
+  p.N = (n_q + 15) / 16 * 32;
   p.tma = p.R % 16 == 0;
   p.q_bytes = (uint32_t)(p.NA * p.N * 128);
   // (+16: without TMA, a token's last group may read past its row)
   p.stage_bytes = (uint32_t)(kTile * p.R + (p.tma ? 0 : 16) + 1023) / 1024 * 1024;
-  p.stages = (int)((kSmemMax - kMiscBytes - p.q_bytes) / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.off_misc = p.q_bytes + p.stages * p.stage_bytes;
+  const int fit = (int)((kSmemMax - kMiscBytes - p.q_bytes) / p.stage_bytes);
+  p.st = Slots(fit, kMaxStages);
+  p.off_misc = p.q_bytes + p.st.n * p.stage_bytes;
   p.total = p.off_misc + kMiscBytes;
   // TMEM: Z buffers of Gp / 2 columns from 0, S buffers of N columns behind them
-  const int zc = p.Gp / 2;
-  p.nz = (512 - (zc + 2 * p.N <= 512 ? 2 : 1) * p.N) / zc;
-  if (p.nz > kMaxZ) p.nz = kMaxZ;
-  p.col_s = p.nz * zc;
-  p.ns = (int)(512 - p.col_s) / p.N;
-  if (p.ns > kMaxS) p.ns = kMaxS;
+  const int zc = p.Gp / 2, zfit = (512 - (zc + 2 * p.N <= 512 ? 2 : 1) * p.N) / zc;
+  p.z = Slots(zfit, kMaxZ);
+  p.col_s = p.z.n * zc;
+  p.s = Slots((int)(512 - p.col_s) / p.N, kMaxS);
+  p.fits = fit >= 1 && zfit >= 1;
   return p;
 }
 
@@ -115,18 +141,35 @@ struct Params {
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t z_ready[kMaxZ], z_free[kMaxZ], s_full[kMaxS], s_free[kMaxS];
-  uint64_t q_full, done, never;
+  uint64_t q_full, done[2], never;
   uint32_t tmem_base, abort;
   __align__(16) float sig[kMaxQ];
   __align__(16) float neg[kMaxQ];  // kAdd: -(log-sum-exp)
-  union {
-    float2 red[4][kMaxQ];          // kLse: per quarter of the lanes
-    float sum[2][kTile];           // kAdd: the second group's share of a token
-  };
+  float2 red[4][kMaxQ];            // kLse: per quarter of the lanes
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
 
-// Pieces [first, pieces) of one token's row -> Z columns; load(u) gives the 16 bytes of piece u.
+// Eight codes -> four words of fp16 subnormals, in levels8's order: word k holds
+// codes k and k + 4 (BITS = 8: 2k and 2k + 1) times 2^(place_of(k) - 24).
+template <int BITS>
+__host__ __device__ constexpr int place_of(int k) {
+  return BITS == 8 ? 0 : BITS == 4 ? 4 * (k & 1) : 2 * k;
+}
+template <int BITS>
+__device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t w2) {
+  if constexpr (BITS == 8) {
+    return make_uint4(__byte_perm(w, 0u, 0x4140), __byte_perm(w, 0u, 0x4342), __byte_perm(w2, 0u, 0x4140),
+                      __byte_perm(w2, 0u, 0x4342));
+  } else if constexpr (BITS == 4) {
+    const uint32_t v = w >> 8;
+    return make_uint4(w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u);
+  } else {
+    const uint32_t v = (w & 0xFFFFu) | (w << 8);  // codes 4-7 beside codes 0-3, 16 bits up
+    return make_uint4(v & 0x00030003u, v & 0x000C000Cu, v & 0x00300030u, v & 0x00C000C0u);
+  }
+}
+
+// The 16-byte pieces [first, pieces) of one token's row -> Z columns; load(u) gives piece u.
 template <int BITS, class F>
 __device__ __forceinline__ void fill_pieces(uint32_t z, int first, int pieces, F load) {
   constexpr int PER = 128 / BITS / 2;  // columns of a piece: 8, 16, 32
@@ -144,9 +187,9 @@ __device__ __forceinline__ void fill_pieces(uint32_t z, int first, int pieces, F
 #pragma unroll
       for (int e = 0; e < PER / 4; ++e) {
         uint4 l;
-        if constexpr (BITS == 8) l = levels8<8>(w[2 * e], w[2 * e + 1]);
-        else if constexpr (BITS == 4) l = levels8<4>(w[e], 0u);
-        else l = levels8<2>(w[e / 2] >> (16 * (e & 1)), 0u);
+        if constexpr (BITS == 8) l = codes8<8>(w[2 * e], w[2 * e + 1]);
+        else if constexpr (BITS == 4) l = codes8<4>(w[e], 0u);
+        else l = codes8<2>(w[e / 2] >> (16 * (e & 1)), 0u);
         o[4 * e] = l.x, o[4 * e + 1] = l.y, o[4 * e + 2] = l.z, o[4 * e + 3] = l.w;
       }
       const uint32_t at = z + (u0 + u) * PER;
@@ -165,12 +208,14 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
 // NC: 8-head chunks a score thread takes (of every other chunk)
 template <int BITS, int NC, Mode MODE>
 __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const __grid_constant__ CUtensorMap tmap, Params p) {
-  constexpr int kDqWarps = Shape<NC>::DQ;
   const Plan pl = plan_of(p.n_q, p.G, BITS);
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc &ms = *reinterpret_cast<Misc *>(smem + pl.off_misc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.G, Gp = pl.Gp, NA = pl.NA, R = pl.R, N = pl.N, stages = pl.stages, nz = pl.nz, ns = pl.ns, n_q = p.n_q;
+  const int G = p.G, Gp = pl.Gp, NA = pl.NA, R = pl.R, n_q = p.n_q;
+  const Slots st = pl.st, zb = pl.z, sb = pl.s;
+  constexpr int N = 32 * NC;  // pl.N
+  constexpr int PARTS = Shape<NC>::PARTS, kDqWarps = Shape<NC>::DQ;
   const int split = blockIdx.x;
   const int64_t b = blockIdx.y;
   // the query prologue has waited for whatever wrote the codes and the lengths
@@ -201,10 +246,11 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     }
     for (int i = 0; i < kMaxS; ++i) {
       mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.s_free[i], 8);
+      mbar_init(&ms.s_free[i], MODE == kAdd ? 4 : 8);
     }
     mbar_init(&ms.q_full, 1);
-    mbar_init(&ms.done, 1);
+    mbar_init(&ms.done[0], 1);
+    mbar_init(&ms.done[1], 1);
     mbar_init(&ms.never, 1);  // completed by nothing: the test-only stall waits on it
     ms.abort = 0u;
     fence_mbar_init();
@@ -213,7 +259,7 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     tmem_alloc(&ms.tmem_base, 512);
     tmem_relinquish();
   }
-  if (tid < n_q) ms.sig[tid] = p.sig[b * n_q + tid];
+  if (tid < kMaxQ) ms.sig[tid] = tid < n_q ? p.sig[b * n_q + tid] : 0.f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -234,24 +280,24 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     bool ok = true;
     const int boxes = pl.tma ? boxes_of(R) : 0;
     int issued = 0;
-    Ring c;
-    for (int i = 0; i < n_tiles; ++i, c.next(stages)) {
-      if (!warp_wait(&ms.empty[c.slot], c.par ^ 1u, abort, kWaitNs)) {
+    for (int i = 0; i < n_tiles; ++i) {
+      if (i >= st.n && !warp_wait(&ms.empty[st.bar(i - st.n)], st.par(i - st.n), abort, kWaitNs)) {
         ok = false;
         break;
       }
-      uint8_t *dst = smem + pl.q_bytes + c.slot * pl.stage_bytes;
+      uint8_t *dst = smem + pl.q_bytes + st.buf(i) * pl.stage_bytes;
+      uint64_t *full = &ms.full[st.bar(i)];
       if (lane == 0) {
         if (rows_of(i) < kTile) {
-          mbar_arrive(&ms.full[c.slot]);  // the dequantising threads read a ragged tile themselves
+          mbar_arrive(full);  // the dequantising threads read a ragged tile themselves
         } else {
-          mbar_arrive_expect_tx(&ms.full[c.slot], (uint32_t)(kTile * R));
+          mbar_arrive_expect_tx(full, (uint32_t)(kTile * R));
           if (pl.tma) {
             const int row0 = (int)(t0 / kTile + tile_of(i)) * R;
             for (int x = 0; x < boxes; ++x)
-              tma_load_3d(dst + x * (R / boxes) * 128, &tmap, 0, row0 + x * (R / boxes), (int)b, &ms.full[c.slot], pol);
+              tma_load_3d(dst + x * (R / boxes) * 128, &tmap, 0, row0 + x * (R / boxes), (int)b, full, pol);
           } else {
-            bulk_g2s_hint(dst, src + (int64_t)tile_of(i) * kTile * R, (uint32_t)(kTile * R), &ms.full[c.slot], pol);
+            bulk_g2s_hint(dst, src + (int64_t)tile_of(i) * kTile * R, (uint32_t)(kTile * R), full, pol);
           }
         }
       }
@@ -259,57 +305,56 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     }
     if (!ok) {
       if (lane == 0) fail();
-      for (int i = max(0, issued - stages); i < issued; ++i)
-        drain_bar(&ms.full[i % stages], (uint32_t)(i / stages) & 1u, kDrainNs);
+      for (int i = max(0, issued - st.n); i < issued; ++i) drain_bar(&ms.full[st.bar(i)], st.par(i), kDrainNs);
       drain_bar(&ms.q_full, 0, kDrainNs);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (whole warp, one lane issues)
-    const uint32_t id_s = idesc_f16(kTile, N, 0, 0);
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers (whole warps, one lane issues):
+    // they take turns at the tiles, so that one's waits and commits (100-200
+    // cycles each) pass while the tensor core has the other's MMAs
+    constexpr uint32_t id_s = idesc_f16(kTile, N, 0, 0);
     const uint32_t b0 = swz_lo(smem_u32(smem), 16), el = elect_one();
-    Ring z, s;
     bool ok = warp_wait(&ms.q_full, 0, abort, kWaitNs);
-    for (int i = 0; ok && i < n_tiles; ++i, z.next(nz), s.next(ns)) {
-      ok = warp_wait(&ms.z_ready[z.slot], z.par, &ms.s_free[s.slot], s.par ^ 1u, abort, kWaitNs);
+    with_count<1, (FSQ_MAX_G + 15) / 16>(Gp / 16, [&](auto ks) {
+    for (int i = warp - 1; ok && i < n_tiles; i += 2) {
+      ok = (i < sb.n || warp_spin(&ms.s_free[sb.bar(i - sb.n)], sb.par(i - sb.n), abort, kWaitNs)) &&
+           warp_spin(&ms.z_ready[zb.bar(i)], zb.par(i), abort, kWaitNs);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tm + pl.col_s + s.slot * N, a = tm + z.slot * (Gp / 2);
+      const uint32_t d = tm + pl.col_s + sb.buf(i) * N, a = tm + zb.buf(i) * (Gp / 2);
 #pragma unroll
-      for (int k = 0; k < (FSQ_MAX_G + 15) / 16; ++k) {  // atoms of 64 coordinates: four MMAs each
-        if (16 * k >= Gp) break;
+      for (int k = 0; k < decltype(ks)::value; ++k)  // atoms of 64 coordinates: four MMAs each
         mma_ts_warp(el, d, a + 8 * k, b0 + (k >> 2) * (N * 8) + 2 * (k & 3), id_s, k > 0 ? 1u : 0u);
-      }
       if (el) {
-        tc_commit(&ms.s_full[s.slot]);
-        tc_commit(&ms.z_free[z.slot]);
+        tc_commit(&ms.s_full[sb.bar(i)]);
+        tc_commit(&ms.z_free[zb.bar(i)]);
       }
       __syncwarp();
     }
+    });
     if (!ok && lane == 0) fail();
     // every issued MMA finishes before TMEM is freed
-    tc_commit_elect(&ms.done);
-    mbar_wait_fixed(&ms.done, 0, kDrainNs);
+    tc_commit_elect(&ms.done[warp - 1]);
+    mbar_wait_fixed(&ms.done[warp - 1], 0, kDrainNs);
   } else if (warp >= 12) {
     // ------------------------------------------------------------ dequantisation: thread = token
     const int t = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    // a warp's share of the row's pieces or groups
-    constexpr int PARTS = kDqWarps / 4;
-    const int dq = (warp - 12) >> 2;
-    auto lo_of = [&](int n) { return (n + PARTS - 1) / PARTS * dq; };
-    auto hi_of = [&](int n) { return min(n, (n + PARTS - 1) / PARTS * (dq + 1)); };
+    const int part = (warp - 12) >> 2;
+    auto lo_of = [&](int n) { return (n + PARTS - 1) / PARTS * part; };  // this warp's share of n
+    auto hi_of = [&](int n) { return min(n, (n + PARTS - 1) / PARTS * (part + 1)); };
     const int units = (G + 7) / 8, align = R % 4 == 0 ? 4 : R % 2 == 0 ? 2 : 1;
-    if (dq == 0 && 4 * units < Gp / 2)  // the group behind the last one stays zero
-      for (int i = 0; i < nz; ++i) tmem_st4(tm + lanes + i * (Gp / 2) + 4 * units, make_uint4(0u, 0u, 0u, 0u));
-    Ring c, z;
-    for (int i = 0; i < n_tiles; ++i, c.next(stages), z.next(nz)) {
-      if (!warp_wait(&ms.full[c.slot], c.par, &ms.z_free[z.slot], z.par ^ 1u, abort, kWaitNs)) {
+    if (part == 0 && 4 * units < Gp / 2)  // the group behind the last one stays zero
+      for (int i = 0; i < zb.n; ++i) tmem_st4(tm + lanes + i * (Gp / 2) + 4 * units, make_uint4(0u, 0u, 0u, 0u));
+    for (int i = 0; i < n_tiles; ++i) {
+      if (!(i < zb.n || warp_spin(&ms.z_free[zb.bar(i - zb.n)], zb.par(i - zb.n), abort, kWaitNs)) ||
+          !warp_spin(&ms.full[st.bar(i)], st.par(i), abort, kWaitNs)) {
         if (lane == 0) fail();
         break;
       }
       tc_fence_after();
-      const uint8_t *stage = smem + pl.q_bytes + c.slot * pl.stage_bytes;
-      const uint32_t zt = tm + lanes + z.slot * (Gp / 2);
+      const uint8_t *stage = smem + pl.q_bytes + st.buf(i) * pl.stage_bytes;
+      const uint32_t zt = tm + lanes + zb.buf(i) * (Gp / 2);
       const int rows = rows_of(i);
       // a ragged tile's rows from memory, the last one again for those behind it
       const uint8_t *row = src + ((int64_t)tile_of(i) * kTile + min(t, rows - 1)) * R;
@@ -330,11 +375,13 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
         for (int u = lo_of(units); u < hi_of(units); ++u) {
           uint4 v;
           if (whole || u + 1 < units) {
-            v = group8<BITS>(row, u, align);
+            uint32_t w[2];
+            group_words<BITS>(row, u, align, w);
+            v = codes8<BITS>(w[0], w[1]);
           } else {  // the last group may reach past the row, and there past the cache: byte by byte
             uint32_t w[2] = {0u, 0u};
             for (int x = 0; x < BITS && u * BITS + x < R; ++x) w[x / 4] |= (uint32_t)row[u * BITS + x] << (8 * (x & 3));
-            v = levels8<BITS>(w[0], w[1]);
+            v = codes8<BITS>(w[0], w[1]);
           }
           tmem_st4(zt + 4 * u, v);
         }
@@ -343,8 +390,8 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ms.z_ready[z.slot]);
-        mbar_arrive(&ms.empty[c.slot]);
+        mbar_arrive(&ms.z_ready[zb.bar(i)]);
+        mbar_arrive(&ms.empty[st.bar(i)]);
       }
     }
   } else if (warp >= 4) {
@@ -352,7 +399,6 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     const int wg = (warp - 4) >> 2, q4 = warp & 3;
     const int r = 32 * q4 + lane;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-    const int chunks = N / 16;
     bool ok = true;
     // test-only stall: a wait that runs out on purpose (nothing completes `never`)
     if (p.stall_ns != 0u && !warp_wait(&ms.never, 0, abort, p.stall_ns)) ok = false;
@@ -379,79 +425,98 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
         }
         if (lane == 0) ms.neg[h] = -(m + log2f(l));
       }
+      if (tid - 4 * 32 < kMaxQ - n_q) ms.neg[n_q + tid - 4 * 32] = -INFINITY;  // heads that pad the last chunk
       named_bar(5, 256);
     }
-    float ref[MODE == kLse ? 8 * NC : 1], sum[MODE == kLse ? 8 * NC : 1];
+    float2 ref[MODE == kLse ? 4 * NC : 1], sum[MODE == kLse ? 4 * NC : 1];  // of two heads each; ref holds its negative
     float *acc = p.acc + b * p.acc_stride + t0;
-    Ring s;
-    for (int i = 0; i < n_tiles; ++i, s.next(ns)) {
-      const bool valid = r < rows_of(i);
-      float old = 0.f;
-      if (MODE == kAdd && wg == 0 && valid) old = acc[(int64_t)tile_of(i) * kTile + r];
-      ok = ok && warp_wait(&ms.s_full[s.slot], s.par, abort, kWaitNs);
+    // kLse: the groups halve the heads of every tile, for whose sums a thread has
+    // no more registers.  kAdd: they take turns at the tiles.  A chunk's scores are
+    // loaded while the one before is worked on.
+    constexpr int STEP = MODE == kAdd ? 2 : 1, CH = MODE == kAdd ? 2 * NC : NC;
+    auto chunk_of = [&](int c) { return MODE == kAdd ? c : 2 * c + wg; };
+    uint32_t v[2][16];
+    int i = MODE == kAdd ? wg : 0;
+    auto fetch = [&](int tile, int c, uint32_t *to) {
+      tmem_ld16(tm + lanes + pl.col_s + sb.buf(tile) * N + 16 * chunk_of(c), to);
+    };
+    auto arrived = [&](int tile) {
+      ok = ok && warp_spin(&ms.s_full[sb.bar(tile)], sb.par(tile), abort, kWaitNs);
       tc_fence_after();
-      float w4[4] = {0.f, 0.f, 0.f, 0.f};
+    };
+    if (i < n_tiles) {
+      arrived(i);
+      fetch(i, 0, v[0]);
+    }
+    for (; ok && i < n_tiles; i += STEP) {
+      const bool valid = r < rows_of(i);
+      float *to = acc + (int64_t)tile_of(i) * kTile + r;
+      float old = 0.f;
+      if (MODE == kAdd && valid) old = *to;
+      float2 w2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int ch = 2 * c + wg;
-        if (ch >= chunks) break;  // uniform
-        uint32_t v[16];
-        tmem_ld16(tm + lanes + pl.col_s + s.slot * N + 16 * ch, v);
+      for (int c = 0; c < CH; ++c) {
+        const int ch = chunk_of(c);
+        uint32_t(&x16)[16] = v[CH % 2 ? 0 : c & 1];
+        tmem_ld_wait16(x16);
+        float2 x[4];  // S_hi + S_lo of two heads each
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = __fadd2_rn(make_float2(__uint_as_float(x16[2 * e]), __uint_as_float(x16[2 * e + 1])),
+                            make_float2(__uint_as_float(x16[8 + 2 * e]), __uint_as_float(x16[9 + 2 * e])));
+        if (c + 1 < CH) {
+          fetch(i, c + 1, v[CH % 2 ? 0 : (c + 1) & 1]);
+        } else {
+          // the tile's scores are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.s_free[sb.bar(i)]);
+          if (i + STEP < n_tiles) {
+            arrived(i + STEP);
+            fetch(i + STEP, 0, v[0]);
+          }
+        }
         float sg[8], ng[8];
         *reinterpret_cast<float4 *>(sg) = *reinterpret_cast<const float4 *>(&ms.sig[8 * ch]);
         *reinterpret_cast<float4 *>(sg + 4) = *reinterpret_cast<const float4 *>(&ms.sig[8 * ch + 4]);
-        if (MODE == kAdd) {
+        if constexpr (MODE == kAdd) {
           *reinterpret_cast<float4 *>(ng) = *reinterpret_cast<const float4 *>(&ms.neg[8 * ch]);
           *reinterpret_cast<float4 *>(ng + 4) = *reinterpret_cast<const float4 *>(&ms.neg[8 * ch + 4]);
-        }
-        tmem_ld_wait();
-        if constexpr (MODE == kAdd) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = fmaf(__uint_as_float(v[e]) + __uint_as_float(v[8 + e]), sg[e], ng[e]);
-            if (8 * ch + e < n_q) w4[e & 3] += ex2_approx(x);
+          for (int e = 0; e < 4; ++e) {
+            const float2 d = __ffma2_rn(x[e], make_float2(sg[2 * e], sg[2 * e + 1]), make_float2(ng[2 * e], ng[2 * e + 1]));
+            w2[e & 1] = __fadd2_rn(w2[e & 1], make_float2(ex2_approx(d.x), ex2_approx(d.y)));
           }
         } else {
-          float d[8], far = -INFINITY;
+          if (i == 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = (__uint_as_float(v[e]) + __uint_as_float(v[8 + e])) * sg[e];
-            if (i == 0) {
-              ref[8 * c + e] = x;
-              sum[8 * c + e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+              ref[4 * c + e] = make_float2(-x[e].x * sg[2 * e], -x[e].y * sg[2 * e + 1]);
+              sum[4 * c + e] = make_float2(0.f, 0.f);
             }
-            d[e] = x - ref[8 * c + e];
-            far = fmaxf(far, d[e]);
+          }
+          float2 d[4];
+          float far = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d[e] = __ffma2_rn(x[e], make_float2(sg[2 * e], sg[2 * e + 1]), ref[4 * c + e]);
+            far = fmax3f(far, d[e].x, d[e].y);
           }
           if (valid) {
             if (far > kFar) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (d[e] > kFar) {
-                  sum[8 * c + e] *= exp2f(-d[e]);
-                  ref[8 * c + e] += d[e];
-                  d[e] = 0.f;
-                }
+              for (int e = 0; e < 4; ++e) {
+                if (d[e].x > kFar) sum[4 * c + e].x *= exp2f(-d[e].x), ref[4 * c + e].x -= d[e].x, d[e].x = 0.f;
+                if (d[e].y > kFar) sum[4 * c + e].y *= exp2f(-d[e].y), ref[4 * c + e].y -= d[e].y, d[e].y = 0.f;
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[8 * c + e] += ex2_approx(d[e]);
+            for (int e = 0; e < 4; ++e)
+              sum[4 * c + e] = __fadd2_rn(sum[4 * c + e], make_float2(ex2_approx(d[e].x), ex2_approx(d[e].y)));
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.s_free[s.slot]);
-      if constexpr (MODE == kAdd) {
-        const float w = (w4[0] + w4[1]) + (w4[2] + w4[3]);
-        if (wg == 1) ms.sum[i & 1][r] = w;
-        if (named_bar_or(1 + q4, 64, !ok)) {
-          ok = false;
-          break;
-        }
-        if (wg == 0 && valid) acc[(int64_t)tile_of(i) * kTile + r] = old + (w + ms.sum[i & 1][r]);
-      } else if (!ok) {
-        break;  // the whole warp
-      }
+      if (MODE == kAdd && valid) *to = old + ((w2[0].x + w2[0].y) + (w2[1].x + w2[1].y));
     }
     if (!ok) fail();
     if constexpr (MODE == kLse) {
@@ -459,10 +524,11 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int ch = 2 * c + wg;
-        if (ch >= chunks) break;
+        if (ch >= N / 16) break;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float l = sum[8 * c + e], m = l == 0.f ? -INFINITY : ref[8 * c + e];  // NaN sums keep their reference
+          const float2 s2 = sum[4 * c + e / 2], r2 = ref[4 * c + e / 2];
+          float l = e % 2 ? s2.y : s2.x, m = l == 0.f ? -INFINITY : -(e % 2 ? r2.y : r2.x);  // NaN sums keep their reference
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
             const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
@@ -532,12 +598,12 @@ __global__ void __launch_bounds__(kAbsorbThreads, 1) weights_query(const uint16_
       sm, q, W_kv, n_q, n_kv, G, NA * kAtom, c, blockIdx.x, b,
       [&](int h, int g, float v, int e) {
         const int ph = (g & ~7) | order_of<BITS>(g & 7), n = (h >> 3) * 16 + (h & 7);
-        const float s = scalbnf(v, kTop - e);
+        const float s = scalbnf(v, kTop - e - place_of<BITS>((ph & 7) / 2));
         const __half hi = __float2half_rn(s);
         *reinterpret_cast<__half *>(at(n, ph)) = hi;
         *reinterpret_cast<__half *>(at(n + 8, ph)) = __float2half_rn(s - __half2float(hi));
       },
-      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop); });
+      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop + 24); });
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -595,7 +661,7 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
   cudaError_t e = launch_pdl(weights_query<BITS>, dim3(n_kv, (unsigned)B), dim3(kAbsorbThreads), 0, st, q, W_kv, p.n_q, n_kv, p.G,
                              pl.NA, pl.N, scale * kLog2e, qbuf, sig, p.err);
   if (e != cudaSuccess) return e;
-  switch ((pl.N / 16 + 1) / 2) {
+  switch (pl.N / 32) {
     case 1: return launch_nc<BITS, 1>(map, p, B, pl, prof, st);
     case 2: return launch_nc<BITS, 2>(map, p, B, pl, prof, st);
     case 3: return launch_nc<BITS, 3>(map, p, B, pl, prof, st);
@@ -609,7 +675,7 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
 bool weights_supported(int n_q, int G, int bits) {
   if (n_q > tc::weights::kMaxQ) return false;
   const tc::weights::Plan p = tc::weights::plan_of(n_q, G, bits);
-  return p.stages >= 1 && p.nz >= 1 && p.ns >= 1;
+  return p.fits;
 }
 int weights_tile_tokens() { return tc::weights::kTile; }
 size_t weights_query_bytes(int n_q, int G, int bits) { return tc::weights::plan_of(n_q, G, bits).q_bytes; }

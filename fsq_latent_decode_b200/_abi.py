@@ -423,28 +423,44 @@ def decode_attn_multi(q, codes, W_kv, T, n_kv, G, code_batch_stride=None, opts=N
     return out
 
 
+# The wrappers of the serving operators are called once per layer and step, at
+# sizes whose kernels take a few microseconds: they check what a raw pointer
+# cannot, with few Python-level calls.
 def _opt_ptr(t):
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _launch(what, stream, *tensors):
+    """The stream to launch on.  The calls run on the current device: tensors that
+    live elsewhere are refused."""
+    import torch
+    dev = tensors[0].get_device()  # -1: not on a GPU
+    for t in tensors:
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {tensors[0].device}")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream() without the Stream object
 
 
 def _heads(t, what):
     """Token stride of a [n_tok, heads, d_h] tensor whose heads lie d_h apart (any token stride)."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]):
         raise ValueError(f"{what} must be [n_tok, heads, d_h] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _vector(t, n, dtype, what):
+    if t is not None and (t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{what} must hold {n} contiguous {dtype} values")
 
 
 def _of_type(t, dtype, what):
-    if t is not None and t.dtype != dtype:
+    if t is not None and t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}")
-
-
-def _on_current_device(what, *tensors):
-    """The calls launch on the current device: refuse tensors that live elsewhere."""
-    import torch
-    for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
-            raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
 
 
 def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, eps=1e-6, rope_base=1.0e6,
@@ -455,49 +471,66 @@ def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, ep
     0, 1, ..).  A decode step passes positions=seq_lens and pos0=-1.  Returns
     q_out, or (q_out, k_out) when k is given; an output may be its own input."""
     import torch
+    bf16 = torch.bfloat16
+    ldq = _heads(q, "q")
     n_tok, n_q, d_h = q.shape
-    for t, what in ((q, "q"), (k, "k"), (q_gain, "q_gain"), (k_gain, "k_gain"), (q_out, "q_out"), (k_out, "k_out")):
-        _of_type(t, torch.bfloat16, what)
-    _of_type(positions, torch.int32, "positions")
-    if k is not None and (k.shape[0] != n_tok or k.shape[2] != d_h):
-        raise ValueError("k must be [n_tok, n_k, d_h] of the same tokens as q")
-    for t, n, what in ((positions, n_tok, "positions"), (q_gain, d_h, "q_gain"), (k_gain, d_h, "k_gain")):
-        if t is not None and (t.numel() != n or not t.is_contiguous()):
-            raise ValueError(f"{what} must hold {n} contiguous values")
+    n_k = ldk = ldko = 0
+    if q.dtype is not bf16:
+        raise ValueError("q must be torch.bfloat16")
     if q_out is None:
-        q_out = torch.empty((n_tok, n_q, d_h), dtype=torch.bfloat16, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("an output must have its input's shape")
-    n_k = 0 if k is None else k.shape[1]
-    ld = [_heads(q, "q"), _heads(q_out, "q_out"), _heads(k, "k") if n_k else 0, _heads(k_out, "k_out") if n_k else 0]
-    _on_current_device("qk_norm_rope", q, k, q_gain, k_gain, positions, q_out, k_out)
-    st = qk_norm_rope_raw(_ptr(q), ld[0], n_q, _opt_ptr(q_gain), _ptr(q_out), ld[1], _opt_ptr(k), ld[2], n_k,
-                          _opt_ptr(k_gain), _opt_ptr(k_out), ld[3], n_tok, d_h, _opt_ptr(positions), int(pos0),
-                          float(eps), float(rope_base), _stream_ptr(stream))
+        q_out = torch.empty((n_tok, n_q, d_h), dtype=bf16, device=q.device)
+    elif q_out.dtype is not bf16 or q_out.shape != q.shape:
+        raise ValueError("q_out must be torch.bfloat16 of q's shape")
+    if k is not None:
+        ldk = _heads(k, "k")
+        if k.dtype is not bf16 or k.shape[0] != n_tok or k.shape[2] != d_h:
+            raise ValueError("k must be torch.bfloat16 [n_tok, n_k, d_h] of the same tokens as q")
+        n_k = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=bf16, device=k.device)
+        elif k_out.dtype is not bf16 or k_out.shape != k.shape:
+            raise ValueError("k_out must be torch.bfloat16 of k's shape")
+        ldko = _heads(k_out, "k_out")
+    _vector(positions, n_tok, torch.int32, "positions")
+    _vector(q_gain, d_h, bf16, "q_gain")
+    _vector(k_gain, d_h, bf16, "k_gain")
+    ldqo = _heads(q_out, "q_out")
+    s = _launch("qk_norm_rope", stream, q, k, q_gain, k_gain, positions, q_out, k_out)
+    st = _lib().fsq_qk_norm_rope(q.data_ptr(), ldq, n_q, _opt_ptr(q_gain), q_out.data_ptr(), ldqo, _opt_ptr(k), ldk, n_k,
+                                 _opt_ptr(k_gain), _opt_ptr(k_out) if n_k else None, ldko, n_tok, d_h,
+                                 _opt_ptr(positions), pos0, eps, rope_base, s)
     _check(st, "fsq_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
 
 
-def _cache_stride(codes, rb, T, what):
+def _cache_stride(codes, rb, B, T, what):
     """Batch stride in bytes of a [B, T_max, R] uint8 cache with contiguous rows."""
-    if codes.dim() != 3 or codes.shape[2] != rb or codes.shape[1] < T or codes.stride(2) != 1 or \
-            (codes.shape[1] > 1 and codes.stride(1) != rb):
-        raise ValueError(f"{what} must be [B, T_max >= {T}, {rb}] uint8 with contiguous rows")
+    import torch
+    shape, st = codes.shape, codes.stride()
+    if codes.dtype is not torch.uint8 or len(shape) != 3 or shape[0] != B or shape[2] != rb or shape[1] < T or \
+            st[2] != 1 or (shape[1] > 1 and st[1] != rb):
+        raise ValueError(f"{what} must be uint8 [{B}, at least {T}, {rb}] with contiguous rows")
     # a size-1 leading dim may carry any stride
-    return codes.stride(0) if codes.shape[0] > 1 else (codes.shape[1] * rb + 15) // 16 * 16
+    return st[0] if B > 1 else (shape[1] * rb + 15) // 16 * 16
+
+
+def _acc_stride(t, B, n, what):
+    """Row stride of a fp32 [B, at least n] tensor with contiguous rows."""
+    import torch
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.float32 or len(shape) != 2 or shape[0] != B or shape[1] < n or (shape[1] > 1 and st[1] != 1):
+        raise ValueError(f"{what} must be fp32 [{B}, at least {n}] with contiguous rows")
+    return st[0] if B > 1 else max(st[0], shape[1])
 
 
 def _attn_inputs(q, W_kv, n_kv, G, opts):
     """Checks q [B, n_q, 128] and W_kv [2 n_kv 128, G], contiguous bf16; returns opts and the row bytes."""
     import torch
-    _of_type(q, torch.bfloat16, "q")
-    _of_type(W_kv, torch.bfloat16, "W_kv")
-    if q.dim() != 3 or not q.is_contiguous():
-        raise ValueError("q must be contiguous [B, n_q, d_h]")
-    if tuple(W_kv.shape) != (2 * n_kv * q.shape[2], G) or not W_kv.is_contiguous():
-        raise ValueError("W_kv must be contiguous [2 * n_kv * d_h, G]")
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or len(shape) != 3 or not q.is_contiguous():
+        raise ValueError("q must be contiguous torch.bfloat16 [B, n_q, d_h]")
+    if W_kv.dtype is not torch.bfloat16 or W_kv.shape != (2 * n_kv * shape[2], G) or not W_kv.is_contiguous():
+        raise ValueError("W_kv must be contiguous torch.bfloat16 [2 * n_kv * d_h, G]")
     if opts is None:
         opts = attn_opts()
     return opts, row_bytes(G, opts.levels or 16)
@@ -510,51 +543,37 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
     import torch
     opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
     B, n_q, d_h = q.shape
-    _of_type(prefix, torch.uint8, "prefix")
-    _of_type(codes, torch.uint8, "codes")
-    if prefix.dim() != 2 or prefix.shape[0] < T_prefix or prefix.shape[1] != rb or not prefix.is_contiguous():
-        raise ValueError(f"prefix must be contiguous [at least {T_prefix}, {rb}]")
-    if T > 0 and (codes is None or codes.shape[0] != B):
+    shape = prefix.shape
+    if prefix.dtype is not torch.uint8 or len(shape) != 2 or shape[0] < T_prefix or shape[1] != rb or \
+            not prefix.is_contiguous():
+        raise ValueError(f"prefix must be contiguous uint8 [at least {T_prefix}, {rb}]")
+    if T > 0 and codes is None:
         raise ValueError("codes must hold the own tokens of every row")
-    stride = _cache_stride(codes, rb, T, "codes") if T > 0 else 0
+    stride = _cache_stride(codes, rb, B, T, "codes") if T > 0 else 0
     dtype = torch.float32 if opts.out_fp32 else torch.bfloat16
-    if out is not None and (out.shape != q.shape or out.dtype != dtype or not out.is_contiguous()):
-        raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
-    _on_current_device("decode_attn_prefix", q, prefix, codes, W_kv, out, *opts._tensors)
     if out is None:
         out = torch.empty((B, n_q, d_h), dtype=dtype, device=q.device)
-    nbytes = prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts)
-    ws = (workspace or Workspace(q.device)).get(nbytes)
-    st = decode_attn_prefix_raw(_ptr(q), B, n_q, d_h, _ptr(prefix), T_prefix, _opt_ptr(codes), stride, T, G, _ptr(W_kv),
-                                n_kv, opts, _ptr(ws), ws.numel(), _ptr(out), _stream_ptr(stream))
+    elif out.shape != q.shape or out.dtype is not dtype or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
+    s = _launch("decode_attn_prefix", stream, q, prefix, codes, W_kv, out, *opts._tensors)
+    ws = (workspace or Workspace(q.device)).get(prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
+    st = decode_attn_prefix_raw(q.data_ptr(), B, n_q, d_h, prefix.data_ptr(), T_prefix, _opt_ptr(codes), stride, T, G,
+                                W_kv.data_ptr(), n_kv, opts, ws.data_ptr(), ws.numel(), out.data_ptr(), s)
     _check(st, "fsq_decode_attn_prefix")
     return out
-
-
-def _acc_stride(t, B, n, what):
-    """Row stride of a [B, at least n] tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be [B, at least {n}] with contiguous rows")
-    return t.stride(0) if B > 1 else max(t.stride(0), t.shape[1])
 
 
 def attn_weights(q, codes, W_kv, acc, T, n_kv, G, opts=None, workspace=None, stream=None):
     """Adds to acc[b, t] (fp32 [B, at least T]) the attention weight of token t of
     codes[b, :T] for the queries q [B, n_q, 128], summed over the heads; with
     opts.seq_lens row b holds that many tokens.  Returns acc."""
-    import torch
     opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
     B, n_q, d_h = q.shape
-    _of_type(codes, torch.uint8, "codes")
-    _of_type(acc, torch.float32, "acc")
-    if codes.shape[0] != B:
-        raise ValueError("codes must hold a row for every query")
-    cs, as_ = _cache_stride(codes, rb, T, "codes"), _acc_stride(acc, B, T, "acc")
-    _on_current_device("attn_weights", q, codes, W_kv, acc, *opts._tensors)
-    nbytes = attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts)
-    ws = (workspace or Workspace(q.device)).get(nbytes)
-    st = attn_weights_raw(_ptr(q), B, n_q, d_h, _ptr(codes), cs, T, G, _ptr(W_kv), n_kv, opts, _ptr(acc), as_, _ptr(ws),
-                          ws.numel(), _stream_ptr(stream))
+    cs, as_ = _cache_stride(codes, rb, B, T, "codes"), _acc_stride(acc, B, T, "acc")
+    s = _launch("attn_weights", stream, q, codes, W_kv, acc, *opts._tensors)
+    ws = (workspace or Workspace(q.device)).get(attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
+    st = attn_weights_raw(q.data_ptr(), B, n_q, d_h, codes.data_ptr(), cs, T, G, W_kv.data_ptr(), n_kv, opts,
+                          acc.data_ptr(), as_, ws.data_ptr(), ws.numel(), s)
     _check(st, "fsq_attn_weights")
     return acc
 
@@ -570,31 +589,24 @@ def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=No
     import torch
     B = codes.shape[0]
     rb = row_bytes(G, levels)
-    _of_type(codes, torch.uint8, "codes")
-    _of_type(acc, torch.float32, "acc")
     if (out is None) != (acc_out is None):
         raise ValueError("out and acc_out go together")
     if out is None:
         out, acc_out = codes, acc
-    _of_type(out, torch.uint8, "out")
-    _of_type(acc_out, torch.float32, "acc_out")
     n_out = T if out is codes else min(T, n_keep)
+    cs, os_ = _cache_stride(codes, rb, B, T, "codes"), _cache_stride(out, rb, B, n_out, "out")
     as_, aos = _acc_stride(acc, B, T, "acc"), _acc_stride(acc_out, B, n_out, "acc_out")
-    if out.shape[0] != B:
-        raise ValueError("out must hold the rows of codes")
-    for t, shape, what in ((seq_lens, (B,), "seq_lens"), (lens_out, (B,), "lens_out"), (kept, (B, n_keep), "kept")):
-        _of_type(t, torch.int32, what)
-        if t is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{what} must be contiguous {shape}")
+    _vector(seq_lens, B, torch.int32, "seq_lens")
+    _vector(lens_out, B, torch.int32, "lens_out")
+    _vector(kept, B * n_keep, torch.int32, "kept")
+    s = _launch("cache_evict", stream, codes, acc, out, acc_out, seq_lens, lens_out, kept)
     nbytes = cache_evict_workspace_size(B, T, G, levels)
     if nbytes == 0:
         raise FsqError(FSQ_ERR_INVALID_ARG, "fsq_cache_evict_workspace_size")
-    cs, os_ = _cache_stride(codes, rb, T, "codes"), _cache_stride(out, rb, n_out, "out")
-    _on_current_device("cache_evict", codes, acc, out, acc_out, seq_lens, lens_out, kept)
     ws = (workspace or Workspace(codes.device)).get(nbytes)
-    st = cache_evict_raw(_ptr(codes), cs, _ptr(acc), as_, _opt_ptr(seq_lens), B, T, n_keep, n_recent, G, levels,
-                         _ptr(out), os_, _ptr(acc_out), aos, _opt_ptr(lens_out), _opt_ptr(kept), _ptr(ws),
-                         ws.numel(), _stream_ptr(stream))
+    st = _lib().fsq_cache_evict(codes.data_ptr(), cs, acc.data_ptr(), as_, _opt_ptr(seq_lens), B, T, n_keep, n_recent, G,
+                                levels, out.data_ptr(), os_, acc_out.data_ptr(), aos, _opt_ptr(lens_out),
+                                _opt_ptr(kept), ws.data_ptr(), ws.numel(), s)
     _check(st, "fsq_cache_evict")
     return out, acc_out
 

@@ -264,8 +264,11 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
     k = (nt + s - 1) / s;
   } else {
     double best = 0;
+    int64_t last = 0;
     for (int s = 1; s <= kNumSMs; ++s) {
       const int64_t kk = (most + s - 1) / s;
+      if (kk == last) continue;
+      last = kk;
       const int64_t sp = (nt + kk - 1) / kk, so = (no + kk - 1) / kk, ctas = QT * sp + Bc * so;
       const double cost = (double)((ctas + kNumSMs - 1) / kNumSMs) * (0.6 * kk + 5.0) +
                           8e-6 / 3.0 * (double)(sp + so) * Bc * n_q * (G + 2);
@@ -319,9 +322,12 @@ fsq_status plan_weights(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G,
     k = (nt + s - 1) / s;
   } else {
     // one CTA per SM runs at a time; a CTA costs its tiles and the start and end of about four
-    int64_t best = 0;
+    int64_t best = 0, last = 0;
     for (int s = 1; s <= kNumSMs; ++s) {
-      const int64_t kk = (nt + s - 1) / s, ctas = Bc * ((nt + kk - 1) / kk);
+      const int64_t kk = (nt + s - 1) / s;
+      if (kk == last) continue;
+      last = kk;
+      const int64_t ctas = Bc * ((nt + kk - 1) / kk);
       const int64_t cost = (ctas + kNumSMs - 1) / kNumSMs * (kk + 4);
       if (s == 1 || cost < best) best = cost, k = kk;
       if (kk == 1) break;

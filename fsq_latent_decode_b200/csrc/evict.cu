@@ -10,7 +10,8 @@
 //                 token that stays, by a radix select over order-preserving
 //                 32-bit keys (digits of 11, 11 and 10 bits: histograms in
 //                 shared memory, each CTA of the cluster adds up a slice of the
-//                 bins over all of them), then writes one keep bit per token
+//                 bins over all of them; up to 131072 tokens the keys stay in
+//                 registers), then writes one keep bit per token
 //                 and each chunk's position in the packed row.
 //  evict_compact  one CTA per chunk of tokens copies its kept rows, weights and
 //                 indices to their places.
@@ -36,9 +37,9 @@ namespace evict {
 constexpr int kNT = 1024;              // threads of a select CTA
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
-constexpr int kPieceTok = kNT;         // tokens a select CTA looks at in one step
+constexpr int kHeld = 16;              // words of a select warp whose keys stay in registers
 constexpr int kCopyNT = 256;           // threads of a compaction CTA
-constexpr int kCopyBytes = 32 * 1024;  // code bytes of a chunk
+constexpr int kCopyBytes = 16 * 1024;  // code bytes of a chunk
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 // Tokens per chunk: a power of two of at least 32 tokens (whole keep words, and
@@ -102,6 +103,7 @@ struct SelectParams {
 // Exclusive prefix of `v` over the CTA's threads; *total: the sum.  red has
 // kNT / 32 entries; two barriers.
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint32_t *total) {
+  static_assert(kNT / 32 == 32, "reads one warp total per lane");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t s = v;
 #pragma unroll
@@ -111,7 +113,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint
   }
   if (lane == 31) red[warp] = s;
   __syncthreads();
-  uint32_t w = red[lane];  // kNT / 32 == 32 warps
+  const uint32_t w = red[lane];
   uint32_t ws = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -124,138 +126,157 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint
   return before + s - v;
 }
 
-__global__ void __launch_bounds__(kNT) evict_select(SelectParams p) {
-  static_assert(kNT / 32 == 32, "block_prefix reads one warp total per lane");
+// The CTA's segment is `per` 32-token words per warp, a warp's words in a row.
+// HELD: per <= kHeld and the keys stay in registers; else they are read again
+// (from L2) in each pass.
+template <bool HELD>
+__global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
   cg::cluster_group cl = cg::this_cluster();
   const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  __shared__ uint32_t hist[kBins];    // this CTA's keys by digit
-  __shared__ uint32_t slice[kMaxCluster];   // per rank: its slice's keys, all CTAs (written by the ranks)
-  __shared__ uint32_t found[2];       // digit and keys still to keep inside it (written by the rank that finds it)
-  __shared__ uint32_t total[kMaxCluster];   // per rank: kept tokens / ties of its segment
+  __shared__ uint32_t hist[kBins];          // this CTA's keys by digit
+  __shared__ uint32_t bin_sum[kBins];       // its slice of the bins over the cluster
+  __shared__ uint32_t slice[kMaxCluster];   // per rank: its slice's keys (written by the ranks)
+  __shared__ uint32_t found[2];             // digit, and keys still to keep inside it (written by the rank that finds it)
+  __shared__ uint32_t total[kMaxCluster];   // per rank: ties, kept tokens of its segment
   __shared__ uint32_t red[32];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.x / CS;
   pdl_wait();
-  const int64_t L = p.lens ? [&]() -> int64_t {
-    const int64_t v = p.lens[b];
-    return v < 0 ? 0 : (v > p.T ? p.T : v);
-  }() : p.T;
-  const bool bad = p.lens && p.lens[b] != L;
+  const int64_t given = p.lens ? p.lens[b] : p.T;
+  const int64_t L = given < 0 ? 0 : (given > p.T ? p.T : given);
   const int64_t after = min(L, p.n_keep);
-  // this CTA's tokens: whole steps, so that they are whole keep words; chunks
-  // are at most one step wide and divide it
-  const int64_t steps = (p.T + kPieceTok - 1) / kPieceTok, per = (steps + CS - 1) / CS;
-  const int64_t s0 = min((int64_t)rank * per * kPieceTok, p.T), s1 = min(s0 + per * kPieceTok, p.T);
+  const int64_t w0 = ((int64_t)rank * 32 + warp) * per;  // this warp's first word
   const float *acc = p.acc + b * p.acc_stride;
-  const int64_t c0 = s0 / p.chunk, c1 = s0 < s1 ? (s1 + p.chunk - 1) / p.chunk : c0;  // and its chunks
-  for (int64_t c = c0 + tid; c < c1; c += kNT) p.flag[b * p.nchunk + c] = 0u;
+  // the segment's chunks (a power of two of words, at most 32 of them)
+  const int cw = p.chunk / 32;
+  for (int64_t c = (int64_t)rank * 32 * per / cw + tid; c < min(p.nchunk, ((int64_t)(rank + 1) * 32 * per + cw - 1) / cw);
+       c += kNT)
+    p.flag[b * p.nchunk + c] = 0u;
   if (blockIdx.x == 0 && tid == 0) {
     *p.ticket = 0u;
     *p.err = 0u;
   }
-  const int64_t N = L - p.n_recent;               // candidates (when the row is cut at all)
-  uint32_t need = 0;                              // candidates to keep
-  uint32_t limit = 0;                             // key of the last one
-  uint32_t ties = 0;                              // of the keys equal to it, how many stay
   const bool cut = L > p.n_keep;
-  if (cut) need = (uint32_t)(p.n_keep - p.n_recent);
-  if (cut && need > 0) {
-    const int64_t e1 = min(s1, N);
+  const int64_t N = cut ? L - p.n_recent : 0;  // candidates
+  const uint32_t need = cut ? (uint32_t)(p.n_keep - p.n_recent) : 0u;  // of which stay
+  uint32_t held[HELD ? kHeld : 1];
+  if constexpr (HELD) {
+    float v[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int64_t t = (w0 + i) * 32 + lane;
+      v[i] = i < per && t < N ? acc[t] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = key_of(v[i]);
+  }
+  // f(i, token, key) for this thread's candidates
+  auto each = [&](auto f) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i < per) f(i, (w0 + i) * 32 + lane, held[i]);
+    } else {
+      for (int i = 0; i < per; ++i) {
+        const int64_t t = (w0 + i) * 32 + lane;
+        f(i, t, t < N ? key_of(acc[t]) : 0u);
+      }
+    }
+  };
+  uint32_t limit = 0, ties = need;  // key of the last one that stays; how many of the keys equal to it do
+  if (need > 0) {
     int shift = 32;
-    uint32_t high = 0;                            // digits found so far, in place
-    ties = need;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int bitsn = pass < 2 ? 11 : 10;
-      const int bins = 1 << bitsn;
+      const int bitsn = pass < 2 ? 11 : 10, bins = 1 << bitsn, sb = bins / CS;
       const uint32_t above = shift == 32 ? 0u : (0xFFFFFFFFu << shift);
       shift -= bitsn;
-      for (int i = tid; i < bins; i += kNT) hist[i] = 0u;
+      for (int i = tid; i < bins; i += kNT) hist[i] = bin_sum[i] = 0u;
       __syncthreads();
-      for (int64_t t = s0 + tid; t < e1; t += kNT) {
-        const uint32_t k = key_of(acc[t]);
-        if ((k & above) == high) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
-      }
+      each([&](int, int64_t t, uint32_t k) {
+        if (t < N && (k & above) == limit) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      });
       cl.sync();
-      // rank r adds up bins [r, r + 1) * bins / CS over the cluster (bins / CS <= 2 kNT)
-      const int sb = bins / CS, b0 = rank * sb;
-      uint32_t mine[2] = {0u, 0u};                // bins 2 tid, 2 tid + 1 of the slice, counted from its top
-      const int hi = b0 + sb - 1;
-      for (int r = 0; r < CS; ++r) {
-        const uint32_t *h = cl.map_shared_rank(hist, r);
-        if (2 * tid < sb) mine[0] += h[hi - 2 * tid];
-        if (2 * tid + 1 < sb) mine[1] += h[hi - 2 * tid - 1];
+      // rank r adds up bins [r, r + 1) * sb over the cluster
+      for (int i = tid; i < bins; i += kNT) {
+        const uint32_t v = cl.map_shared_rank(hist, i / sb)[rank * sb + i % sb];
+        if (v) atomicAdd(&bin_sum[i % sb], v);
       }
+      __syncthreads();
+      // two bins a thread, from the slice's top
+      const int hi = sb - 1 - 2 * tid;
+      const uint32_t m0 = hi >= 0 ? bin_sum[hi] : 0u, m1 = hi >= 1 ? bin_sum[hi - 1] : 0u;
       uint32_t sum;
-      const uint32_t before = block_prefix(mine[0] + mine[1], red, &sum);
+      const uint32_t before = block_prefix(m0 + m1, red, &sum);
       if (tid < CS) cl.map_shared_rank(slice, tid)[rank] = sum;
       cl.sync();
-      uint32_t higher = 0;                        // keys in the slices above this one
+      uint32_t higher = 0;  // keys in the slices above this one
       for (int r = rank + 1; r < CS; ++r) higher += slice[r];
-      const uint32_t n0 = higher + before, n1 = n0 + mine[0], n2 = n1 + mine[1];
+      const uint32_t n0 = higher + before, n1 = n0 + m0, n2 = n1 + m1;
       const int at = (n0 < ties && ties <= n1) ? 0 : (n1 < ties && ties <= n2) ? 1 : -1;
-      if (at >= 0) {                              // one thread of the cluster
-        const uint32_t digit = (uint32_t)(hi - 2 * tid - at), left = ties - (at ? n1 : n0);
+      if (at >= 0)  // one thread of the cluster
         for (int r = 0; r < CS; ++r) {
           uint32_t *f = cl.map_shared_rank(found, r);
-          f[0] = digit;
-          f[1] = left;
+          f[0] = (uint32_t)(rank * sb + hi - at);
+          f[1] = ties - (at ? n1 : n0);
         }
-      }
       cl.sync();
-      high |= found[0] << shift;
+      limit |= found[0] << shift;
       ties = found[1];
     }
-    limit = high;
   }
-  // keep bits: above the limit, or equal to it and among the first `ties`; the recent tokens
-  auto state = [&](int64_t t) -> int {            // 0 goes, 1 stays, 2 stays if its turn among the ties comes
-    if (t >= L) return 0;
-    if (!cut || t >= N) return 1;
-    if (need == 0) return 0;
-    const uint32_t k = key_of(acc[t]);
-    return k > limit ? 1 : k == limit ? 2 : 0;
-  };
-  uint32_t eq_before = 0;                         // ties in the segments before this one
-  if (cut && need > 0) {
-    uint32_t eq = 0;
-    for (int64_t t = s0 + tid; t < min(s1, N); t += kNT) eq += key_of(acc[t]) == limit ? 1u : 0u;
-    uint32_t sum;
-    block_prefix(eq, red, &sum);
+  // ties before this warp's tokens
+  uint32_t eq_before = 0;
+  if (need > 0) {
+    uint32_t eq = 0, sum;
+    each([&](int, int64_t t, uint32_t k) { eq += t < N && k == limit ? 1u : 0u; });
+    eq = block_prefix(eq, red, &sum);
+    eq_before = __shfl_sync(0xffffffffu, eq, 0);
     if (tid < CS) cl.map_shared_rank(total, tid)[rank] = sum;
     cl.sync();
     for (int r = 0; r < rank; ++r) eq_before += total[r];
     cl.sync();
   }
-  // first pass over the segment: keep words and this segment's kept tokens before each chunk
-  uint32_t run = 0;
-  for (int64_t base = s0; base < s1; base += kPieceTok) {
-    const int64_t t = base + tid;
-    const int st = t < s1 ? state(t) : 0;
-    bool keep = st == 1;
-    if (cut && need > 0) {
-      uint32_t sum;
-      const uint32_t eq = block_prefix(st == 2 ? 1u : 0u, red, &sum);
-      keep = keep || (st == 2 && eq_before + eq < ties);
-      eq_before += sum;
+  // keep words: a candidate above the limit, or equal to it and among the first
+  // `ties`; every token from N to L.  Lane i keeps the i-th word of a round of 32.
+  uint32_t kept = 0;  // of the warp, so far
+  uint32_t mine = 0;
+  auto flush = [&](int64_t word0, int n) {  // words word0 .. word0 + n - 1 are in lanes 0 .. n - 1
+    const int64_t w = word0 + lane;
+    uint32_t c = lane < n ? __popc(mine) : 0u, s = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
     }
-    const uint32_t word = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0 && t < p.words * 32) p.bits[b * p.words + t / 32] = word;
-    uint32_t sum;
-    const uint32_t pre = block_prefix(keep ? 1u : 0u, red, &sum);
-    if (tid % p.chunk == 0 && t < s1) p.off[b * p.nchunk + t / p.chunk] = (int32_t)(run + pre);
-    run += sum;
-  }
-  if (tid < CS) cl.map_shared_rank(total, tid)[rank] = run;
+    if (lane < n && w < p.words) {
+      p.bits[b * p.words + w] = mine;
+      if (w % cw == 0) p.off[b * p.nchunk + w / cw] = (int32_t)(kept + s - c);  // within the warp, so far
+    }
+    kept += __shfl_sync(0xffffffffu, s, 31);
+  };
+  each([&](int i, int64_t t, uint32_t k) {
+    const bool same = need > 0 && t < N && k == limit;
+    const uint32_t eq = __ballot_sync(0xffffffffu, same);
+    const bool first = same && eq_before + __popc(eq & ((1u << lane) - 1u)) < ties;
+    eq_before += __popc(eq);
+    const uint32_t word = __ballot_sync(0xffffffffu, t < L && (t >= N || first || (need > 0 && k > limit)));
+    if (lane == (i & 31)) mine = word;
+    if ((i & 31) == 31 || i == per - 1) flush(w0 + (i & ~31), (i & 31) + 1);
+  });
+  uint32_t sum;
+  uint32_t base = block_prefix(lane == 0 ? kept : 0u, red, &sum);  // kept tokens of the warps before this one
+  base = __shfl_sync(0xffffffffu, base, 0);
+  if (tid < CS) cl.map_shared_rank(total, tid)[rank] = sum;
   cl.sync();
-  uint32_t before = 0;
-  for (int r = 0; r < rank; ++r) before += total[r];
-  for (int64_t c = c0 + tid; c < c1; c += kNT) p.off[b * p.nchunk + c] += (int32_t)before;
+  for (int r = 0; r < rank; ++r) base += total[r];
+  for (int64_t w = (w0 + cw - 1) / cw * cw + (int64_t)lane * cw; w < min(p.words, w0 + per); w += 32 * cw)
+    p.off[b * p.nchunk + w / cw] += (int32_t)base;
   // every CTA of the cluster has read lens[b], which lens_out may alias
   if (rank == 0 && tid == 0) {
     p.rows[3 * b] = (int32_t)L;
     p.rows[3 * b + 1] = (int32_t)after;
-    p.rows[3 * b + 2] = bad ? 1 : 0;
+    p.rows[3 * b + 2] = given != L ? 1 : 0;
     if (p.lens_out) p.lens_out[b] = (int32_t)after;
   }
   if (p.kept)
@@ -348,12 +369,14 @@ __global__ void __launch_bounds__(kCopyNT) evict_compact(CopyParams p) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) av[k] = tid + k * kCopyNT < n ? acc[list[tid + k * kCopyNT]] : 0.f;
   uint4 v[U == 16 ? kRegs : 1];
-  const int ppr = p.R / U;          // pieces per row
   if constexpr (U == 16) {
+    const int ppr = p.R / 16;       // pieces per row
+    const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 1024 (kCopyBytes / 16)
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
       const int i = tid + k * kCopyNT;
-      if (i < n * ppr) v[k] = *reinterpret_cast<const uint4 *>(src + (int64_t)list[i / ppr] * p.R + (i % ppr) * 16);
+      const int r = (int)((uint32_t)i * inv >> 16);
+      if (i < n * ppr) v[k] = *reinterpret_cast<const uint4 *>(src + (int64_t)list[r] * p.R + (i - r * ppr) * 16);
     }
   } else {
     const int nb = rows_here * p.R;  // the row's bytes may end inside a 16-byte piece
@@ -386,6 +409,7 @@ __global__ void __launch_bounds__(kCopyNT) evict_compact(CopyParams p) {
   // ---- store
   uint8_t *to = p.out + b * p.ostride + dst * p.R;
   if constexpr (U == 16) {
+    const int ppr = p.R / 16;
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
       const int i = tid + k * kCopyNT;
@@ -460,9 +484,11 @@ cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc
   SelectParams sp{acc, acc_stride, lens, T, n_keep, n_recent, (int32_t *)(ws + pl.off_rows),
                   (uint32_t *)(ws + pl.off_bits), (int32_t *)(ws + pl.off_off), (uint32_t *)(ws + pl.off_flag),
                   (uint32_t *)(ws + pl.off_ticket), (uint32_t *)ws, lens_out, kept, pl.nchunk, pl.words, pl.chunk};
-  // one CTA of the cluster per four steps of tokens
+  // words per warp, with as many CTAs as give each four or fewer
+  const int64_t words = (T + 31) / 32;
   int cs = 1;
-  while (cs < kMaxCluster && T > (int64_t)cs * 4 * kPieceTok) cs *= 2;
+  while (cs < kMaxCluster && words > (int64_t)cs * 32 * 4) cs *= 2;
+  const int per = (int)((words + 32 * cs - 1) / (32 * cs));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * cs));
   cfg.blockDim = dim3(kNT);
@@ -475,7 +501,7 @@ cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, sp);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, per <= kHeld ? evict_select<true> : evict_select<false>, sp, per);
   if (e != cudaSuccess) return e;
   CopyParams cp{codes, out, bstride, ostride, acc, acc_out, acc_stride, acc_ostride, kept, sp.rows, sp.bits, sp.off,
                 sp.flag, sp.ticket, (uint32_t *)ws, B, n_keep, pl.nchunk, pl.words, R, pl.chunk, out == codes};

@@ -124,8 +124,12 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint
                              uint16_t *k_out, int64_t ldko, int64_t n_tok, const int32_t *positions, int64_t pos0,
                              float eps, float rope_base, cudaStream_t st) {
   NormRopeParams p;
-  for (int i = 0; i < kHalf; ++i)
-    p.turn[i] = pow((double)rope_base, -2.0 * i / FSQ_HEAD_DIM) / (2.0 * 3.14159265358979323846);
+  double fine[8];  // base^(-2i/128) = base^(-16 (i / 8) / 128) base^(-2 (i % 8) / 128)
+  for (int i = 0; i < 8; ++i) fine[i] = pow((double)rope_base, -2.0 * i / FSQ_HEAD_DIM);
+  for (int i = 0; i < kHalf; i += 8) {
+    const double coarse = pow((double)rope_base, -2.0 * i / FSQ_HEAD_DIM) / (2.0 * 3.14159265358979323846);
+    for (int k = 0; k < 8; ++k) p.turn[i + k] = coarse * fine[k];
+  }
   p.x[0] = q, p.x[1] = k;
   p.y[0] = q_out, p.y[1] = k_out;
   p.ldx[0] = ldq, p.ldx[1] = ldk;

@@ -9,9 +9,8 @@
 //  evict_select   one thread-block cluster per row finds the weight of the last
 //                 token that stays, by a radix select over order-preserving
 //                 32-bit keys (digits of 11, 11 and 10 bits: histograms in
-//                 shared memory, each CTA of the cluster adds up a slice of the
-//                 bins over all of them; up to 131072 tokens the keys stay in
-//                 registers), then writes one keep bit per token
+//                 shared memory, added up over the cluster; up to 131072 tokens
+//                 the keys stay in registers), then writes one keep bit per token
 //                 and each chunk's position in the packed row.
 //  evict_compact  one CTA per chunk of tokens copies its kept rows, weights and
 //                 indices to their places.
@@ -34,12 +33,11 @@ namespace cg = cooperative_groups;
 namespace fsq {
 namespace evict {
 
-constexpr int kNT = 1024;              // threads of a select CTA
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
-constexpr int kHeld = 16;              // words of a select warp whose keys stay in registers
+constexpr int kHeld = 32;              // most words of a select warp whose keys stay in registers
 constexpr int kCopyNT = 256;           // threads of a compaction CTA
-constexpr int kCopyBytes = 16 * 1024;  // code bytes of a chunk
+constexpr int kCopyBytes = 32 * 1024;  // code bytes of a chunk
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 // Tokens per chunk: a power of two of at least 32 tokens (whole keep words, and
@@ -100,10 +98,11 @@ struct SelectParams {
   int chunk;
 };
 
-// Exclusive prefix of `v` over the CTA's threads; *total: the sum.  red has
-// kNT / 32 entries; two barriers.
+// Exclusive prefix of `v` over the CTA's NT threads; *total: the sum.  red has
+// NT / 32 entries; two barriers.
+template <int NT>
 __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint32_t *total) {
-  static_assert(kNT / 32 == 32, "reads one warp total per lane");
+  static_assert(NT / 32 <= 32, "reads one warp total per lane");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t s = v;
 #pragma unroll
@@ -113,44 +112,49 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *red, uint
   }
   if (lane == 31) red[warp] = s;
   __syncthreads();
-  const uint32_t w = red[lane];
+  const uint32_t w = lane < NT / 32 ? red[lane] : 0u;
   uint32_t ws = w;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < NT / 32; o <<= 1) {
     const uint32_t n = __shfl_up_sync(0xffffffffu, ws, o);
     if (lane >= o) ws += n;
   }
-  *total = __shfl_sync(0xffffffffu, ws, 31);
+  *total = __shfl_sync(0xffffffffu, ws, NT / 32 - 1);
   const uint32_t before = __shfl_sync(0xffffffffu, ws - w, warp);
   __syncthreads();
   return before + s - v;
 }
 
 // The CTA's segment is `per` 32-token words per warp, a warp's words in a row.
-// HELD: per <= kHeld and the keys stay in registers; else they are read again
-// (from L2) in each pass.
-template <bool HELD>
-__global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
+// HELD: per <= HELD and the keys stay in registers; 0: they are read again
+// (from L2) in each pass.  Latency counts: every CTA sums all bins of the cluster
+// itself, so that a pass has one cluster barrier, and each pass has a histogram of
+// its own; one CTA's worth of tokens takes 256 threads, whose barriers are quick.
+template <int NT, int HELD>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select(SelectParams p, int per) {
+  constexpr int NW = NT / 32, BPT = kBins / NT;  // bins per thread
   cg::cluster_group cl = cg::this_cluster();
   const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  __shared__ uint32_t hist[kBins];          // this CTA's keys by digit
-  __shared__ uint32_t bin_sum[kBins];       // its slice of the bins over the cluster
-  __shared__ uint32_t slice[kMaxCluster];   // per rank: its slice's keys (written by the ranks)
-  __shared__ uint32_t found[2];             // digit, and keys still to keep inside it (written by the rank that finds it)
-  __shared__ uint32_t total[kMaxCluster];   // per rank: ties, kept tokens of its segment
+  __shared__ __align__(16) uint32_t hist[3][kBins];  // per pass: this CTA's keys by digit
+  __shared__ uint32_t found[3];                       // digit, keys still to keep inside it, keys inside it
+  __shared__ uint32_t total[2][kMaxCluster];          // per rank: ties, kept tokens of its segment (written by the ranks)
   __shared__ uint32_t red[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.x / CS;
+  auto sync = [&]() {
+    if (CS > 1) cl.sync();
+    else __syncthreads();
+  };
   pdl_wait();
   const int64_t given = p.lens ? p.lens[b] : p.T;
   const int64_t L = given < 0 ? 0 : (given > p.T ? p.T : given);
   const int64_t after = min(L, p.n_keep);
-  const int64_t w0 = ((int64_t)rank * 32 + warp) * per;  // this warp's first word
+  const int64_t w0 = ((int64_t)rank * NW + warp) * per;  // this warp's first word
   const float *acc = p.acc + b * p.acc_stride;
   // the segment's chunks (a power of two of words, at most 32 of them)
   const int cw = p.chunk / 32;
-  for (int64_t c = (int64_t)rank * 32 * per / cw + tid; c < min(p.nchunk, ((int64_t)(rank + 1) * 32 * per + cw - 1) / cw);
-       c += kNT)
+  for (int64_t c = (int64_t)rank * NW * per / cw + tid; c < min(p.nchunk, ((int64_t)(rank + 1) * NW * per + cw - 1) / cw);
+       c += NT)
     p.flag[b * p.nchunk + c] = 0u;
   if (blockIdx.x == 0 && tid == 0) {
     *p.ticket = 0u;
@@ -159,22 +163,22 @@ __global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
   const bool cut = L > p.n_keep;
   const int64_t N = cut ? L - p.n_recent : 0;  // candidates
   const uint32_t need = cut ? (uint32_t)(p.n_keep - p.n_recent) : 0u;  // of which stay
-  uint32_t held[HELD ? kHeld : 1];
-  if constexpr (HELD) {
-    float v[kHeld];
+  uint32_t held[HELD ? HELD : 1];
+  if constexpr (HELD > 0) {
+    float v[HELD];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
+    for (int i = 0; i < HELD; ++i) {
       const int64_t t = (w0 + i) * 32 + lane;
       v[i] = i < per && t < N ? acc[t] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = key_of(v[i]);
+    for (int i = 0; i < HELD; ++i) held[i] = key_of(v[i]);
   }
   // f(i, token, key) for this thread's candidates
   auto each = [&](auto f) {
-    if constexpr (HELD) {
+    if constexpr (HELD > 0) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i)
+      for (int i = 0; i < HELD; ++i)
         if (i < per) f(i, (w0 + i) * 32 + lane, held[i]);
     } else {
       for (int i = 0; i < per; ++i) {
@@ -183,59 +187,73 @@ __global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
       }
     }
   };
-  uint32_t limit = 0, ties = need;  // key of the last one that stays; how many of the keys equal to it do
+  uint32_t limit = 0, ties = need, equal = need;  // key of the last one that stays; how many of the keys equal to it do, of how many
   if (need > 0) {
     int shift = 32;
+    for (int i = tid; i < 3 * kBins; i += NT) hist[0][i] = 0u;
+    __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int bitsn = pass < 2 ? 11 : 10, bins = 1 << bitsn, sb = bins / CS;
+      const int bitsn = pass < 2 ? 11 : 10, bins = 1 << bitsn;  // the last pass leaves the upper half of the bins empty
       const uint32_t above = shift == 32 ? 0u : (0xFFFFFFFFu << shift);
       shift -= bitsn;
-      for (int i = tid; i < bins; i += kNT) hist[i] = bin_sum[i] = 0u;
-      __syncthreads();
+      uint32_t *h = hist[pass];
       each([&](int, int64_t t, uint32_t k) {
-        if (t < N && (k & above) == limit) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+        if (t < N && (k & above) == limit) atomicAdd(&h[(k >> shift) & (bins - 1)], 1u);
       });
-      cl.sync();
-      // rank r adds up bins [r, r + 1) * sb over the cluster
-      for (int i = tid; i < bins; i += kNT) {
-        const uint32_t v = cl.map_shared_rank(hist, i / sb)[rank * sb + i % sb];
-        if (v) atomicAdd(&bin_sum[i % sb], v);
+      sync();
+      // BPT bins a thread, from the top
+      const int hi = kBins - BPT * (tid + 1);
+      uint32_t m[BPT] = {};
+#pragma unroll
+      for (int r0 = 0; r0 < kMaxCluster; r0 += 4) {  // four CTAs' bins in flight
+        uint4 v[4][BPT / 4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int x = 0; x < BPT / 4; ++x)
+            v[r][x] = r0 + r < CS ? *reinterpret_cast<const uint4 *>(cl.map_shared_rank(h, r0 + r) + hi + 4 * x)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int x = 0; x < BPT / 4; ++x)
+            m[4 * x] += v[r][x].x, m[4 * x + 1] += v[r][x].y, m[4 * x + 2] += v[r][x].z, m[4 * x + 3] += v[r][x].w;
+      }
+      uint32_t mine = 0, sum;
+#pragma unroll
+      for (int x = 0; x < BPT; ++x) mine += m[x];
+      uint32_t n = block_prefix<NT>(mine, red, &sum);  // keys in the bins above this thread's
+      if (n < ties && ties <= n + mine) {  // one thread
+#pragma unroll
+        for (int x = BPT - 1; x >= 0; --x) {
+          if (n < ties && ties <= n + m[x]) {
+            found[0] = (uint32_t)(hi + x);
+            found[1] = ties - n;
+            found[2] = m[x];
+          }
+          n += m[x];
+        }
       }
       __syncthreads();
-      // two bins a thread, from the slice's top
-      const int hi = sb - 1 - 2 * tid;
-      const uint32_t m0 = hi >= 0 ? bin_sum[hi] : 0u, m1 = hi >= 1 ? bin_sum[hi - 1] : 0u;
-      uint32_t sum;
-      const uint32_t before = block_prefix(m0 + m1, red, &sum);
-      if (tid < CS) cl.map_shared_rank(slice, tid)[rank] = sum;
-      cl.sync();
-      uint32_t higher = 0;  // keys in the slices above this one
-      for (int r = rank + 1; r < CS; ++r) higher += slice[r];
-      const uint32_t n0 = higher + before, n1 = n0 + m0, n2 = n1 + m1;
-      const int at = (n0 < ties && ties <= n1) ? 0 : (n1 < ties && ties <= n2) ? 1 : -1;
-      if (at >= 0)  // one thread of the cluster
-        for (int r = 0; r < CS; ++r) {
-          uint32_t *f = cl.map_shared_rank(found, r);
-          f[0] = (uint32_t)(rank * sb + hi - at);
-          f[1] = ties - (at ? n1 : n0);
-        }
-      cl.sync();
       limit |= found[0] << shift;
       ties = found[1];
+      equal = found[2];
+      __syncthreads();
     }
   }
-  // ties before this warp's tokens
+  // ties before this warp's tokens, where not all of them stay
   uint32_t eq_before = 0;
-  if (need > 0) {
+  if (ties < equal) {
     uint32_t eq = 0, sum;
     each([&](int, int64_t t, uint32_t k) { eq += t < N && k == limit ? 1u : 0u; });
-    eq = block_prefix(eq, red, &sum);
+    eq = block_prefix<NT>(eq, red, &sum);
     eq_before = __shfl_sync(0xffffffffu, eq, 0);
-    if (tid < CS) cl.map_shared_rank(total, tid)[rank] = sum;
-    cl.sync();
-    for (int r = 0; r < rank; ++r) eq_before += total[r];
-    cl.sync();
+    if (CS > 1) {
+      if (tid < CS) cl.map_shared_rank(total[0], tid)[rank] = sum;
+      cl.sync();
+      for (int r = 0; r < rank; ++r) eq_before += total[0][r];
+    }
   }
   // keep words: a candidate above the limit, or equal to it and among the first
   // `ties`; every token from N to L.  Lane i keeps the i-th word of a round of 32.
@@ -265,14 +283,15 @@ __global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
     if ((i & 31) == 31 || i == per - 1) flush(w0 + (i & ~31), (i & 31) + 1);
   });
   uint32_t sum;
-  uint32_t base = block_prefix(lane == 0 ? kept : 0u, red, &sum);  // kept tokens of the warps before this one
+  uint32_t base = block_prefix<NT>(lane == 0 ? kept : 0u, red, &sum);  // kept tokens of the warps before this one
   base = __shfl_sync(0xffffffffu, base, 0);
-  if (tid < CS) cl.map_shared_rank(total, tid)[rank] = sum;
-  cl.sync();
-  for (int r = 0; r < rank; ++r) base += total[r];
+  if (CS > 1) {
+    if (tid < CS) cl.map_shared_rank(total[1], tid)[rank] = sum;
+    cl.sync();  // also: every CTA of the cluster has read lens[b], which lens_out may alias, and the others' histograms
+    for (int r = 0; r < rank; ++r) base += total[1][r];
+  }
   for (int64_t w = (w0 + cw - 1) / cw * cw + (int64_t)lane * cw; w < min(p.words, w0 + per); w += 32 * cw)
     p.off[b * p.nchunk + w / cw] += (int32_t)base;
-  // every CTA of the cluster has read lens[b], which lens_out may alias
   if (rank == 0 && tid == 0) {
     p.rows[3 * b] = (int32_t)L;
     p.rows[3 * b + 1] = (int32_t)after;
@@ -280,8 +299,7 @@ __global__ void __launch_bounds__(kNT) evict_select(SelectParams p, int per) {
     if (p.lens_out) p.lens_out[b] = (int32_t)after;
   }
   if (p.kept)
-    for (int64_t i = after + (int64_t)rank * kNT + tid; i < p.n_keep; i += (int64_t)CS * kNT) p.kept[b * p.n_keep + i] = -1;
-  cl.sync();  // no CTA leaves while another may still write its shared memory
+    for (int64_t i = after + (int64_t)rank * NT + tid; i < p.n_keep; i += (int64_t)CS * NT) p.kept[b * p.n_keep + i] = -1;
 }
 
 struct CopyParams {
@@ -296,7 +314,7 @@ struct CopyParams {
   const uint32_t *bits;
   const int32_t *off;
   uint32_t *flag, *ticket, *err;
-  int64_t B, n_keep, nchunk, words;
+  int64_t B, T, n_keep, nchunk, words;
   int R, chunk, in_place;
 };
 
@@ -314,64 +332,69 @@ __device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
 // ones, into registers; others come with their whole chunk into shared memory
 // (aligned, contiguous loads), and the packed bytes are put together there.
 template <int U>
-__global__ void __launch_bounds__(kCopyNT) evict_compact(CopyParams p) {
+__global__ void __launch_bounds__(kCopyNT, 4) evict_compact(CopyParams p) {
   extern __shared__ __align__(16) uint8_t stage[];  // U < 16: the chunk's code bytes
   __shared__ uint16_t list[1024];                   // kept tokens of the chunk
-  __shared__ uint32_t wcnt[32];
   __shared__ uint32_t order;
   __shared__ int go;
   const int tid = threadIdx.x;
   pdl_wait();
-  int64_t job = blockIdx.x;
+  uint32_t job = blockIdx.x;
   if (p.in_place) {
     if (tid == 0) order = atomicAdd(p.ticket, 1u);
     __syncthreads();
     job = order;
   }
   // rows side by side, chunks ascending
-  const int64_t b = job % p.B, c = job / p.B;
+  const int64_t c = job / (uint32_t)p.B, b = job - c * (uint32_t)p.B;
+  const int64_t t0 = (int64_t)c * p.chunk;
+  // all that does not depend on one another in flight together: the row's lengths,
+  // the chunk's place, its keep words (lane = word, in every warp) and its weights
+  const int nw = p.chunk / 32, lane = tid & 31;
   const int64_t L = p.rows[3 * b], after = p.rows[3 * b + 1];
-  if (c == 0 && tid == 0 && p.rows[3 * b + 2]) record_error(p.err, FSQ_ERR_INVALID_ARG);  // the word is clear by now
-  const int64_t t0 = c * p.chunk;
+  const int bad = p.rows[3 * b + 2];
+  const int64_t dst = p.off[b * p.nchunk + c];
+  const uint32_t word = lane < nw ? p.bits[b * p.words + t0 / 32 + lane] : 0u;
+  const float *acc = p.acc + b * p.acc_stride + t0;
+  float av[4];  // of tokens tid + k kCopyNT; chunk <= 4 kCopyNT
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid + k * kCopyNT;
+    av[k] = t < p.chunk && t0 + t < p.T ? acc[t] : 0.f;
+  }
+  if (c == 0 && tid == 0 && bad) record_error(p.err, FSQ_ERR_INVALID_ARG);  // the word is clear by now
   if (t0 >= L) return;  // nothing here; nobody waits for a chunk behind the last token
   const bool still = p.in_place && L == after;  // nothing moves
-  const int64_t dst = p.off[b * p.nchunk + c];
-  // the chunk's kept tokens, ascending
-  const uint32_t *bits = p.bits + b * p.words + t0 / 32;
-  const int nw = p.chunk / 32;
-  if (tid < 32) {
-    const uint32_t n = tid < nw ? __popc(bits[tid]) : 0u;
-    uint32_t s = n;
+  // every warp: kept tokens before each word; then the chunk's kept tokens, ascending
+  uint32_t upto = __popc(word);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, s, o);
-      if (tid >= o) s += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const int n = (int)__shfl_sync(0xffffffffu, upto, 31);
+  int rank[4];  // of this thread's tokens among the kept ones, -1: not kept
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tid + k * kCopyNT, w = t / 32;  // w < 32: the warp's word
+    const uint32_t bits = __shfl_sync(0xffffffffu, word, w), to = __shfl_sync(0xffffffffu, upto, w);
+    rank[k] = -1;
+    if (t < p.chunk && ((bits >> lane) & 1u)) {
+      rank[k] = (int)(to - __popc(bits >> lane));
+      list[rank[k]] = (uint16_t)t;
+      if (p.kept) p.kept[b * p.n_keep + dst + rank[k]] = (int32_t)(t0 + t);
     }
-    wcnt[tid] = s;
   }
-  __syncthreads();
-  for (int t = tid; t < p.chunk; t += kCopyNT) {
-    const uint32_t w = bits[t / 32];
-    if ((w >> (t % 32)) & 1u)
-      list[(t >= 32 ? wcnt[t / 32 - 1] : 0u) + __popc(w & ((1u << (t % 32)) - 1u))] = (uint16_t)t;
-  }
-  __syncthreads();
-  const int n = (int)wcnt[nw - 1];
-  const float *acc = p.acc + b * p.acc_stride + t0;
-  if (p.kept)
-    for (int i = tid; i < n; i += kCopyNT) p.kept[b * p.n_keep + dst + i] = (int32_t)(t0 + list[i]);
   if (still) return;
+  __syncthreads();
   // ---- load
   constexpr int kRegs = kCopyBytes / 16 / kCopyNT;  // 16-byte pieces of a thread
   const uint8_t *src = p.codes + b * p.bstride + t0 * p.R;
   const int rows_here = (int)min((int64_t)p.chunk, L - t0);
-  float av[4];  // chunk <= 4 kCopyNT
-#pragma unroll
-  for (int k = 0; k < 4; ++k) av[k] = tid + k * kCopyNT < n ? acc[list[tid + k * kCopyNT]] : 0.f;
   uint4 v[U == 16 ? kRegs : 1];
   if constexpr (U == 16) {
     const int ppr = p.R / 16;       // pieces per row
-    const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 1024 (kCopyBytes / 16)
+    const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 2048 (kCopyBytes / 16)
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
       const int i = tid + k * kCopyNT;
@@ -455,7 +478,7 @@ __global__ void __launch_bounds__(kCopyNT) evict_compact(CopyParams p) {
   float *ao = p.acc_out + b * p.acc_ostride;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (tid + k * kCopyNT < n) ao[dst + tid + k * kCopyNT] = av[k];
+    if (rank[k] >= 0) ao[dst + rank[k]] = av[k];
   // in place, the freed positions start from zero weight; they are this chunk's own
   if (p.in_place)
     for (int t = tid; t < rows_here; t += kCopyNT)
@@ -484,14 +507,21 @@ cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc
   SelectParams sp{acc, acc_stride, lens, T, n_keep, n_recent, (int32_t *)(ws + pl.off_rows),
                   (uint32_t *)(ws + pl.off_bits), (int32_t *)(ws + pl.off_off), (uint32_t *)(ws + pl.off_flag),
                   (uint32_t *)(ws + pl.off_ticket), (uint32_t *)ws, lens_out, kept, pl.nchunk, pl.words, pl.chunk};
-  // words per warp, with as many CTAs as give each four or fewer
-  const int64_t words = (T + 31) / 32;
+  // words per warp: 256 threads while that keeps the keys in registers, then CTAs
+  // of 512 that do.  (Two of those share an SM, so that 16 clusters of 8 run at once
+  // whatever the GPCs' sizes; of 1024 threads some waited for a second wave.)
+  const int64_t words = pl.words;  // whole chunks
+  const int nt = words <= 8 * 8 ? 256 : 512, nw = nt / 32;
   int cs = 1;
-  while (cs < kMaxCluster && words > (int64_t)cs * 32 * 4) cs *= 2;
-  const int per = (int)((words + 32 * cs - 1) / (32 * cs));
+  while (nt == 512 && cs < kMaxCluster && words > (int64_t)cs * nw * (cs < 4 ? 8 : kHeld)) cs *= 2;
+  const int per = (int)((words + nw * cs - 1) / (nw * cs));
+  auto select = nt == 256      ? evict_select<256, 8>
+                : per <= 16    ? evict_select<512, 16>
+                : per <= kHeld ? evict_select<512, kHeld>
+                               : evict_select<512, 0>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * cs));
-  cfg.blockDim = dim3(kNT);
+  cfg.blockDim = dim3(nt);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -501,10 +531,10 @@ cudaError_t launch_evict(const uint8_t *codes, int64_t bstride, const float *acc
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, per <= kHeld ? evict_select<true> : evict_select<false>, sp, per);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select, sp, per);
   if (e != cudaSuccess) return e;
   CopyParams cp{codes, out, bstride, ostride, acc, acc_out, acc_stride, acc_ostride, kept, sp.rows, sp.bits, sp.off,
-                sp.flag, sp.ticket, (uint32_t *)ws, B, n_keep, pl.nchunk, pl.words, R, pl.chunk, out == codes};
+                sp.flag, sp.ticket, (uint32_t *)ws, B, T, n_keep, pl.nchunk, pl.words, R, pl.chunk, out == codes};
   if (R % 16 == 0 && pl.chunk * R <= kCopyBytes) return launch_copy<16>(cp, st);
   if (R % 8 == 0) return launch_copy<8>(cp, st);
   if (R % 4 == 0) return launch_copy<4>(cp, st);

@@ -9,10 +9,10 @@
 // flops.  Half a warp owns a head: lane i of 16 holds elements 4i .. 4i+3 and
 // their partners 64 + 4i .. 64 + 4i+3, so a pair never leaves its thread, every
 // access is 8 bytes of a contiguous 128, and the mean is four shuffles.  The
-// angles of a token are shared by all of its heads: a CTA forms them once, in
-// turns p * (base^(-2i/128) / 2 pi) in 64 bits, drops the whole turns and calls
-// sincospif on the rest, so a far position loses nothing to the range
-// reduction.
+// angles of a token are shared by all of its heads and formed once, in turns
+// p * (base^(-2i/128) / 2 pi) in 64 bits: without its whole turns the rest goes to
+// sincospif, so a far position loses nothing to the range reduction.  The first
+// heads are loaded before the angles are formed, the next before these are stored.
 #include <math.h>
 
 #include "common.cuh"
@@ -45,77 +45,90 @@ __device__ __forceinline__ uint32_t f32_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// TT tokens per CTA (grid x), hpc heads of each (grid y).
-template <int TT>
-__global__ void __launch_bounds__(kNT) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int hpc) {
-  __shared__ float2 cs[TT][kHalf];  // (cos, sin)
+// A warp works on one token, two heads at a time.  WIDE: a CTA has 8 tokens, a
+// warp all heads of one.  Otherwise a CTA has 16 heads of one token (grid y), a
+// warp two of them.
+template <bool WIDE>
+__global__ void __launch_bounds__(kNT) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int W = kNT / 32, TT = WIDE ? W : 1;
+  __shared__ __align__(16) float2 cs[TT][kHalf];  // (cos, sin)
   __shared__ __align__(16) float gain[2][FSQ_HEAD_DIM];
-  const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * TT;
-  const int nt = (int)min((int64_t)TT, p.n_tok - t0);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t tok = (int64_t)blockIdx.x * TT + (WIDE ? warp : 0);
   const int heads = p.heads[0] + p.heads[1];
-  const int h0 = blockIdx.y * hpc, nh = min(hpc, heads - h0);
+  const int l = lane % 16, side = lane / 16;  // the half-warp's head of a pair
+  const int first = WIDE ? 0 : 2 * (blockIdx.y * W + warp), last = WIDE ? heads : min(heads, first + 2);
+  constexpr int U = WIDE ? kUnroll : 1;
+  const bool there = tok < p.n_tok;
+  const uint16_t *x0 = p.x[0] + tok * p.ldx[0] + 4 * l, *x1 = p.x[1] + tok * p.ldx[1] + 4 * l - p.heads[0] * FSQ_HEAD_DIM;
+  uint16_t *y0 = p.y[0] + tok * p.ldy[0] + 4 * l, *y1 = p.y[1] + tok * p.ldy[1] + 4 * l - p.heads[0] * FSQ_HEAD_DIM;
+  uint2 lo[U], hi[U];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + 2 * u;
+      lo[u] = hi[u] = make_uint2(0u, 0u);
+      if (there && h < last) {
+        const uint16_t *src = (h >= p.heads[0] ? x1 : x0) + h * FSQ_HEAD_DIM;
+        lo[u] = *reinterpret_cast<const uint2 *>(src);
+        hi[u] = *reinterpret_cast<const uint2 *>(src + kHalf);
+      }
+    }
+  };
   pdl_wait();  // x may come from the kernel before this one
+  load(first + side);
   {
     const int w = tid / FSQ_HEAD_DIM, d = tid % FSQ_HEAD_DIM;  // kNT == 2 * FSQ_HEAD_DIM
     gain[w][d] = p.gain[w] ? bf16_to_f32(p.gain[w][d]) : 1.f;
   }
-  for (int i = tid; i < nt * kHalf; i += kNT) {
-    const int t = i / kHalf, k = i % kHalf;
-    const int64_t pos = p.pos0 + (p.positions ? (int64_t)p.positions[t0 + t] : t0 + t);
-    double a = (double)pos * p.turn[k];
-    a -= rint(a);
-    float s, c;
-    sincospif(2.f * (float)a, &s, &c);
-    cs[t][k] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int slot = tid / 16, l = tid % 16;
-  const int items = nt * nh;
-  for (int i0 = slot; i0 < items; i0 += kSlots * kUnroll) {
-    uint2 lo[kUnroll], hi[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int it = i0 + u * kSlots;
-      lo[u] = hi[u] = make_uint2(0u, 0u);
-      if (it < items) {
-        const int t = it / nh, h = h0 + it % nh, w = h >= p.heads[0];
-        const uint16_t *src = p.x[w] + (t0 + t) * p.ldx[w] + (int64_t)(w ? h - p.heads[0] : h) * FSQ_HEAD_DIM;
-        lo[u] = *reinterpret_cast<const uint2 *>(src + 4 * l);
-        hi[u] = *reinterpret_cast<const uint2 *>(src + kHalf + 4 * l);
-      }
+  if (there)
+    for (int k = WIDE ? lane : tid; k < kHalf; k += WIDE ? 32 : kNT) {
+      const int64_t pos = p.pos0 + (p.positions ? (int64_t)p.positions[tok] : tok);
+      double a = (double)pos * p.turn[k];
+      a -= rint(a);
+      float s, c;
+      sincospif(2.f * (float)a, &s, &c);
+      cs[WIDE ? warp : 0][k] = make_float2(c, s);
     }
+  __syncthreads();
+  if (!there) return;
+  const float4 c01 = *reinterpret_cast<const float4 *>(&cs[WIDE ? warp : 0][4 * l]);
+  const float4 c23 = *reinterpret_cast<const float4 *>(&cs[WIDE ? warp : 0][4 * l + 2]);
+  for (int h0 = first + side; h0 - side < last; h0 += 2 * U) {
+    uint2 ol[U], oh[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int it = i0 + u * kSlots;
+    for (int u = 0; u < U; ++u) {
+      const int w = h0 + 2 * u >= p.heads[0];
       const float2 a0 = bf16x2_f32(lo[u].x), a1 = bf16x2_f32(lo[u].y);
       const float2 b0 = bf16x2_f32(hi[u].x), b1 = bf16x2_f32(hi[u].y);
       float ss = a0.x * a0.x + a0.y * a0.y + a1.x * a1.x + a1.y * a1.y;
       ss += b0.x * b0.x + b0.y * b0.y + b1.x * b1.x + b1.y * b1.y;
 #pragma unroll
       for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (it < items) {
-        const int t = it / nh, h = h0 + it % nh, w = h >= p.heads[0];
-        const float r = rsqrtf(fmaf(ss, 1.f / FSQ_HEAD_DIM, p.eps));
-        const float4 ga = *reinterpret_cast<const float4 *>(&gain[w][4 * l]);
-        const float4 gb = *reinterpret_cast<const float4 *>(&gain[w][kHalf + 4 * l]);
-        const float4 c01 = *reinterpret_cast<const float4 *>(&cs[t][4 * l]);
-        const float4 c23 = *reinterpret_cast<const float4 *>(&cs[t][4 * l + 2]);
-        const float x0 = a0.x * r * ga.x, x1 = a0.y * r * ga.y, x2 = a1.x * r * ga.z, x3 = a1.y * r * ga.w;
-        const float y0 = b0.x * r * gb.x, y1 = b0.y * r * gb.y, y2 = b1.x * r * gb.z, y3 = b1.y * r * gb.w;
-        uint16_t *dst = p.y[w] + (t0 + t) * p.ldy[w] + (int64_t)(w ? h - p.heads[0] : h) * FSQ_HEAD_DIM;
-        *reinterpret_cast<uint2 *>(dst + 4 * l) =
-            make_uint2(f32_bf16x2(x0 * c01.x - y0 * c01.y, x1 * c01.z - y1 * c01.w),
-                       f32_bf16x2(x2 * c23.x - y2 * c23.y, x3 * c23.z - y3 * c23.w));
-        *reinterpret_cast<uint2 *>(dst + kHalf + 4 * l) =
-            make_uint2(f32_bf16x2(x0 * c01.y + y0 * c01.x, x1 * c01.w + y1 * c01.z),
-                       f32_bf16x2(x2 * c23.y + y2 * c23.x, x3 * c23.w + y3 * c23.z));
+      const float r = rsqrtf(fmaf(ss, 1.f / FSQ_HEAD_DIM, p.eps));
+      const float4 ga = *reinterpret_cast<const float4 *>(&gain[w][4 * l]);
+      const float4 gb = *reinterpret_cast<const float4 *>(&gain[w][kHalf + 4 * l]);
+      const float x0 = a0.x * r * ga.x, x1 = a0.y * r * ga.y, x2 = a1.x * r * ga.z, x3 = a1.y * r * ga.w;
+      const float y0 = b0.x * r * gb.x, y1 = b0.y * r * gb.y, y2 = b1.x * r * gb.z, y3 = b1.y * r * gb.w;
+      ol[u] = make_uint2(f32_bf16x2(x0 * c01.x - y0 * c01.y, x1 * c01.z - y1 * c01.w),
+                         f32_bf16x2(x2 * c23.x - y2 * c23.y, x3 * c23.z - y3 * c23.w));
+      oh[u] = make_uint2(f32_bf16x2(x0 * c01.y + y0 * c01.x, x1 * c01.w + y1 * c01.z),
+                         f32_bf16x2(x2 * c23.y + y2 * c23.x, x3 * c23.w + y3 * c23.z));
+    }
+    if (h0 - side + 2 * U < last) load(h0 + 2 * U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + 2 * u;
+      if (h < last) {
+        uint16_t *dst = (h >= p.heads[0] ? y1 : y0) + h * FSQ_HEAD_DIM;
+        *reinterpret_cast<uint2 *>(dst) = ol[u];
+        *reinterpret_cast<uint2 *>(dst + kHalf) = oh[u];
       }
     }
   }
 }
 
-constexpr int kTokBig = 8;  // tokens per CTA once they fill the SMs several times over
+constexpr int kWideFrom = 8 * kNumSMs;  // tokens from which CTAs of 8 fill the SMs
 
 }  // namespace
 
@@ -140,13 +153,11 @@ cudaError_t launch_norm_rope(const uint16_t *q, int64_t ldq, int n_q, const uint
   p.pos0 = pos0;
   p.positions = positions;
   p.eps = eps;
-  const int heads = n_q + n_k;
-  if (n_tok >= (int64_t)kTokBig * kNumSMs)
-    return launch_pdl(norm_rope_kernel<kTokBig>, dim3((unsigned)((n_tok + kTokBig - 1) / kTokBig)), dim3(kNT), 0, st,
-                      p, heads);
-  // few tokens: a CTA per token and 16 heads, so that the work spreads over the SMs
-  return launch_pdl(norm_rope_kernel<1>, dim3((unsigned)n_tok, (unsigned)((heads + kSlots - 1) / kSlots)), dim3(kNT),
-                    0, st, p, kSlots);
+  if (n_tok >= kWideFrom)
+    return launch_pdl(norm_rope_kernel<true>, dim3((unsigned)((n_tok + kNT / 32 - 1) / (kNT / 32))), dim3(kNT), 0, st, p);
+  // few tokens: the heads of one over several CTAs, so that the work spreads over the SMs
+  return launch_pdl(norm_rope_kernel<false>, dim3((unsigned)n_tok, (unsigned)((n_q + n_k + kSlots - 1) / kSlots)),
+                    dim3(kNT), 0, st, p);
 }
 
 }  // namespace fsq

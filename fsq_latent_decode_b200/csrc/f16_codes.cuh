@@ -35,25 +35,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b0, uint32_t p0, uint64_t *b
   return __all_sync(0xffffffffu, wait_bars(b0, p0, b1, p1, abort, limit_ns));
 }
 
-// The same, testing the phase for about a microsecond before the warp parks: for
-// the hand-offs of a tile, where the wake-up of a parked warp is what counts.
-__device__ __forceinline__ bool warp_spin(uint64_t *b, uint32_t par, volatile uint32_t *abort, uint64_t limit_ns) {
-  const uint32_t a = smem_u32(b);
-  bool ok = false;
-#pragma unroll 1
-  for (int i = 0; i < 1 && !ok; ++i) ok = __all_sync(0xffffffffu, bar_test(a, par));
-  return ok || warp_wait(b, par, abort, limit_ns);
-}
-
-__device__ __forceinline__ bool warp_spin(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1,
-                                          volatile uint32_t *abort, uint64_t limit_ns) {
-  const uint32_t a0 = smem_u32(b0), a1 = smem_u32(b1);
-  bool ok = false;
-#pragma unroll 1
-  for (int i = 0; i < 1 && !ok; ++i) ok = __all_sync(0xffffffffu, bar_test2(a0, p0, a1, p1));
-  return ok || warp_wait(b0, p0, b1, p1, abort, limit_ns);
-}
-
 // Waits for this thread's tcgen05.ld's; the registers they fill may not be used
 // before, also where other work stands between a load and its wait.
 #define FSQ_RW8(a, o) "+r"(a[o + 0]), "+r"(a[o + 1]), "+r"(a[o + 2]), "+r"(a[o + 3]), "+r"(a[o + 4]), "+r"(a[o + 5]), "+r"(a[o + 6]), "+r"(a[o + 7])

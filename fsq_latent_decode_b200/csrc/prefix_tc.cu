@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       with_count<1, kMaxG / 16>(Gp / 16, [&](auto ks) {
       Ring z, s;
       for (int i = 0; ok && i < n_tiles; ++i, z.next(nz), s.next(ns)) {
-        ok = warp_spin(&ms.s_free[s.slot], s.par ^ 1u, &ms.z_ready[z.slot], z.par, abort, kWaitNs);
+        ok = warp_wait(&ms.s_free[s.slot], s.par ^ 1u, &ms.z_ready[z.slot], z.par, abort, kWaitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tm + pl.col_s + s.slot * kTile, a = tm + pl.col_q;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     } else {
       Ring z, pr;
       for (int i = 0; i < n_tiles; ++i, z.next(nz), pr.next(2)) {
-        ok = warp_spin(&ms.p_ready[pr.slot], pr.par, abort, kWaitNs);
+        ok = warp_wait(&ms.p_ready[pr.slot], pr.par, abort, kWaitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = tm + pl.col_p + pr.slot * (kTile / 2);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     Ring cr, zr;
     for (int i = 0; i < n_tiles; ++i, cr.next(stages), zr.next(nz)) {
       if ((i & 1) != grp) continue;
-      if (!warp_spin(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
+      if (!warp_wait(&ms.full[cr.slot], cr.par, &ms.z_free[zr.slot], zr.par ^ 1u, abort, kWaitNs)) {
         if (lane == 0) fail();
         break;
       }
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     if (wg == 1) sr.next(ns), zp.next(nz);
     else zo.next(nz);
     for (int i = wg; ok && i < n_tiles; i += 2) {
-      ok = warp_spin(&ms.s_full[wg], (uint32_t)(i >> 1) & 1u, abort, kWaitNs);
+      ok = warp_wait(&ms.s_full[wg], (uint32_t)(i >> 1) & 1u, abort, kWaitNs);
       tc_fence_after();
       uint32_t s[64];
       float top = -INFINITY;
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
         top = fmaxf(fmaxf(t2[0], t2[1]), fmaxf(t2[2], t2[3])) * sig;
       }
       // the row's reference after the tile before this one, which the other warp has decided
-      if (i > 0) ok = warp_spin(&ms.decided[wg ^ 1][q4], (uint32_t)((i - 1) >> 1) & 1u, abort, kWaitNs) && ok;
+      if (i > 0) ok = warp_wait(&ms.decided[wg ^ 1][q4], (uint32_t)((i - 1) >> 1) & 1u, abort, kWaitNs) && ok;
       const float was = *(volatile float *)&ms.m[r];
       const bool raise = live && (top > was + kTau || (i == 0 && top > was));
       const float now = raise ? top : was;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       m = now;
       // P(i - 2) has been pooled (a warp without live rows waits too: its arrival
       // for this tile must not count for that one)
-      if (i > 1) ok = warp_spin(&ms.z_free[zp.slot], zp.par, abort, kWaitNs) && ok;
+      if (i > 1) ok = warp_wait(&ms.z_free[zp.slot], zp.par, abort, kWaitNs) && ok;
       tc_fence_after();
       if (busy) {
         const uint32_t tp = tm + lanes + pl.col_p + wg * (kTile / 2);
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
         if (move) {
           // O holds every earlier tile once the last pooling is done
           const float f = raise ? exp2f(was - now) : 1.f;
-          ok = warp_spin(&ms.z_free[zo.slot], zo.par, abort, kWaitNs) && ok;
+          ok = warp_wait(&ms.z_free[zo.slot], zo.par, abort, kWaitNs) && ok;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < Gp; c += 32) {

@@ -11,11 +11,11 @@
 //
 // The result is a running fp32 sum over many steps, so scores are exact to fp32:
 // Q' = W_k^T q * scale * log2 e is held as two fp16 terms per head (22 bits),
-// scaled by a power of two, against the codes n themselves: the level offset
-// -L/2 moves all of a head's scores alike, which the softmax does not see.  A
-// code stays where it lies in its word, as the mantissa of an fp16 subnormal
-// (n 2^-24 times the power of two of its place, which Q' takes off): one LOP3 per
-// pair.
+// scaled by a power of two, against the codes n themselves (4 and 8 bits): the
+// level offset -L/2 moves all of a head's scores alike, which the softmax does not
+// see.  A code stays where it lies in its word, as the mantissa of an fp16
+// subnormal (n 2^-24 times the power of two of its place, which Q' takes off): one
+// LOP3 per pair.
 //   S [128 tokens x 2 n_q] = Z [128 x G] . [Q'_hi ; Q'_lo]^T      score = S_hi + S_lo
 // A token is a TMEM lane, so a softmax thread owns its tokens: kLse keeps
 // (reference, sum) per head and thread, the first token's score as the
@@ -149,11 +149,17 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
 
-// Eight codes -> four words of fp16 subnormals, in levels8's order: word k holds
-// codes k and k + 4 (BITS = 8: 2k and 2k + 1) times 2^(place_of(k) - 24).
+// Eight codes -> four words of the score's A operand, in levels8's order.  BITS = 4
+// and 8: word k holds codes k and k + 4 (BITS = 8: 2k and 2k + 1) as subnormals,
+// times 2^(place_of(k) - 24).  BITS = 2: levels.  (The offset of two-bit codes is
+// large beside their scores, and the sums, truncated at its size, lose half a digit.)
 template <int BITS>
 __host__ __device__ constexpr int place_of(int k) {
-  return BITS == 8 ? 0 : BITS == 4 ? 4 * (k & 1) : 2 * k;
+  return BITS == 4 ? 4 * (k & 1) : 0;
+}
+template <int BITS>
+__host__ __device__ constexpr int unit_of() {
+  return BITS == 2 ? 0 : 24;
 }
 template <int BITS>
 __device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t w2) {
@@ -164,8 +170,7 @@ __device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t w2) {
     const uint32_t v = w >> 8;
     return make_uint4(w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u);
   } else {
-    const uint32_t v = (w & 0xFFFFu) | (w << 8);  // codes 4-7 beside codes 0-3, 16 bits up
-    return make_uint4(v & 0x00030003u, v & 0x000C000Cu, v & 0x00300030u, v & 0x00C000C0u);
+    return levels8<2>(w, 0u);
   }
 }
 
@@ -317,8 +322,8 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     bool ok = warp_wait(&ms.q_full, 0, abort, kWaitNs);
     with_count<1, (FSQ_MAX_G + 15) / 16>(Gp / 16, [&](auto ks) {
     for (int i = warp - 1; ok && i < n_tiles; i += 2) {
-      ok = (i < sb.n || warp_spin(&ms.s_free[sb.bar(i - sb.n)], sb.par(i - sb.n), abort, kWaitNs)) &&
-           warp_spin(&ms.z_ready[zb.bar(i)], zb.par(i), abort, kWaitNs);
+      ok = (i < sb.n || warp_wait(&ms.s_free[sb.bar(i - sb.n)], sb.par(i - sb.n), abort, kWaitNs)) &&
+           warp_wait(&ms.z_ready[zb.bar(i)], zb.par(i), abort, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tm + pl.col_s + sb.buf(i) * N, a = tm + zb.buf(i) * (Gp / 2);
@@ -347,8 +352,8 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     if (part == 0 && 4 * units < Gp / 2)  // the group behind the last one stays zero
       for (int i = 0; i < zb.n; ++i) tmem_st4(tm + lanes + i * (Gp / 2) + 4 * units, make_uint4(0u, 0u, 0u, 0u));
     for (int i = 0; i < n_tiles; ++i) {
-      if (!(i < zb.n || warp_spin(&ms.z_free[zb.bar(i - zb.n)], zb.par(i - zb.n), abort, kWaitNs)) ||
-          !warp_spin(&ms.full[st.bar(i)], st.par(i), abort, kWaitNs)) {
+      if (!(i < zb.n || warp_wait(&ms.z_free[zb.bar(i - zb.n)], zb.par(i - zb.n), abort, kWaitNs)) ||
+          !warp_wait(&ms.full[st.bar(i)], st.par(i), abort, kWaitNs)) {
         if (lane == 0) fail();
         break;
       }
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
       tmem_ld16(tm + lanes + pl.col_s + sb.buf(tile) * N + 16 * chunk_of(c), to);
     };
     auto arrived = [&](int tile) {
-      ok = ok && warp_spin(&ms.s_full[sb.bar(tile)], sb.par(tile), abort, kWaitNs);
+      ok = ok && warp_wait(&ms.s_full[sb.bar(tile)], sb.par(tile), abort, kWaitNs);
       tc_fence_after();
     };
     if (i < n_tiles) {
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(kAbsorbThreads, 1) weights_query(const uint16_
         *reinterpret_cast<__half *>(at(n, ph)) = hi;
         *reinterpret_cast<__half *>(at(n + 8, ph)) = __float2half_rn(s - __half2float(hi));
       },
-      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop + 24); });
+      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop + unit_of<BITS>()); });
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {

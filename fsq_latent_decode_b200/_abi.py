@@ -524,7 +524,8 @@ def _acc_stride(t, B, n, what):
 
 
 def _attn_inputs(q, W_kv, n_kv, G, opts):
-    """Checks q [B, n_q, 128] and W_kv [2 n_kv 128, G], contiguous bf16; returns opts and the row bytes."""
+    """Checks q [B, n_q, 128] and W_kv [2 n_kv 128, G], contiguous bf16, and the
+    lengths; returns opts, the row bytes and the lengths."""
     import torch
     shape = q.shape
     if q.dtype is not torch.bfloat16 or len(shape) != 3 or not q.is_contiguous():
@@ -533,7 +534,9 @@ def _attn_inputs(q, W_kv, n_kv, G, opts):
         raise ValueError("W_kv must be contiguous torch.bfloat16 [2 * n_kv * d_h, G]")
     if opts is None:
         opts = attn_opts()
-    return opts, row_bytes(G, opts.levels or 16)
+    held = getattr(opts, "_tensors", (None, None))  # opts made by attn_opts: its tensors
+    _vector(held[1], shape[0], torch.int32, "opts.seq_lens")
+    return opts, row_bytes(G, opts.levels or 16), held[1]
 
 
 def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, workspace=None, out=None, stream=None):
@@ -541,7 +544,7 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
     (uint8 [T.., R]) and continue with their own codes[b, :T] (opts.seq_lens[b]
     of them, 0 included; codes may be None when T is 0).  Absorbed form."""
     import torch
-    opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
+    opts, rb, lens = _attn_inputs(q, W_kv, n_kv, G, opts)
     B, n_q, d_h = q.shape
     shape = prefix.shape
     if prefix.dtype is not torch.uint8 or len(shape) != 2 or shape[0] < T_prefix or shape[1] != rb or \
@@ -555,7 +558,7 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
         out = torch.empty((B, n_q, d_h), dtype=dtype, device=q.device)
     elif out.shape != q.shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
-    s = _launch("decode_attn_prefix", stream, q, prefix, codes, W_kv, out, *opts._tensors)
+    s = _launch("decode_attn_prefix", stream, q, prefix, codes, W_kv, out, lens)
     ws = (workspace or Workspace(q.device)).get(prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
     st = decode_attn_prefix_raw(q.data_ptr(), B, n_q, d_h, prefix.data_ptr(), T_prefix, _opt_ptr(codes), stride, T, G,
                                 W_kv.data_ptr(), n_kv, opts, ws.data_ptr(), ws.numel(), out.data_ptr(), s)
@@ -567,10 +570,10 @@ def attn_weights(q, codes, W_kv, acc, T, n_kv, G, opts=None, workspace=None, str
     """Adds to acc[b, t] (fp32 [B, at least T]) the attention weight of token t of
     codes[b, :T] for the queries q [B, n_q, 128], summed over the heads; with
     opts.seq_lens row b holds that many tokens.  Returns acc."""
-    opts, rb = _attn_inputs(q, W_kv, n_kv, G, opts)
+    opts, rb, lens = _attn_inputs(q, W_kv, n_kv, G, opts)
     B, n_q, d_h = q.shape
     cs, as_ = _cache_stride(codes, rb, B, T, "codes"), _acc_stride(acc, B, T, "acc")
-    s = _launch("attn_weights", stream, q, codes, W_kv, acc, *opts._tensors)
+    s = _launch("attn_weights", stream, q, codes, W_kv, acc, lens)
     ws = (workspace or Workspace(q.device)).get(attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
     st = attn_weights_raw(q.data_ptr(), B, n_q, d_h, codes.data_ptr(), cs, T, G, W_kv.data_ptr(), n_kv, opts,
                           acc.data_ptr(), as_, ws.data_ptr(), ws.numel(), s)

@@ -198,6 +198,8 @@ def test_attention_wrapper_refusals():
                  lambda: F.decode_attn_prefix(q.float(), prefix, codes, W, 50, 30, 8, 84),
                  lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 30, 8, 84, out=torch.zeros(2, 16, 128)),
                  lambda: F.decode_attn_prefix(q, prefix, codes, W, 50, 30, 8, 84),
+                 lambda: F.attn_weights(q, codes, W, acc, 30, 8, 84, opts=F.attn_opts(seq_lens=torch.ones(3, dtype=torch.int32))),
+                 lambda: F.attn_weights(q, codes, W, acc, 30, 8, 84, opts=F.attn_opts(seq_lens=torch.ones(2, dtype=torch.int64))),
                  lambda: F.attn_weights(q, codes, W, acc, 31, 8, 84), lambda: F.attn_weights(q, codes, W, acc.T, 30, 8, 84),
                  lambda: F.attn_weights(q, codes[:1], W, acc, 30, 8, 84),
                  lambda: F.attn_weights(q[:, :, :64], codes, W, acc, 30, 8, 84),

@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       if (align == 16) {
         // 16 bytes of a row at a time, in order, so that the reads are contiguous
         // over the warp.  Eight lanes then hold neighbouring pieces of one token,
-        // whose chunks of the same rank share banks: each lane starts at another
-        // of its NE chunks, and the eight writes of a step cover all banks.
+        // whose chunks of the same rank share banks: each lane takes its NE chunks
+        // in another order, and the eight writes of a step cover all banks.
         constexpr int NE = 16 / BITS;                  // chunks (groups of 8 coordinates) of a piece
         const int ppr = R / 16;
         const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 64 * 16
@@ -331,24 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
         for (int x = dt; x < kTile * ppr; x += kDqWarps * 32) {
           const int t = (int)(((uint32_t)x * inv) >> 16), piece = x - t * ppr;
           const uint4 v = *reinterpret_cast<const uint4 *>(c + 16 * x);
-          const int rot = (piece * NE >> 3) & (NE - 1);
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};        // rotated right by rot groups
-          {
-            const int by = rot * BITS / 4;             // whole words
-            if (by & 1) {
-              const uint32_t f = w[0];
-              w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = f;
-            }
-            if (by & 2) {
-              const uint32_t f = w[0], g = w[1];
-              w[0] = w[2], w[1] = w[3], w[2] = f, w[3] = g;
-            }
-            if constexpr (BITS == 2) {                 // and half of one
-              const uint32_t sh = 16u * (rot & 1), f = w[0];
+          // chunk e ^ rot is the lane's e-th; its place: atom, row, and the
+          // chunk's number swizzled by the row
+          const int c0 = NE * piece, rot = (c0 >> 3) & (NE - 1);
+          const uint32_t at = (uint32_t)((c0 >> 3) * kAtomBytes + t * 128 + (((c0 & 7) ^ (t & 7) ^ rot) << 4));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if constexpr (BITS == 2) {
+            if (rot & 1) {
 #pragma unroll
-              for (int e = 0; e < 3; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], sh);
-              w[3] = __funnelshift_r(w[3], f, sh);
+              for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e], 16);
             }
+          }
+          constexpr int ONE = BITS == 8 ? 0 : BITS == 4 ? 1 : 2, TWO = BITS == 8 ? 1 : BITS == 4 ? 2 : 4;  // rot bits
+          if (rot & ONE) {
+            uint32_t f = w[0];
+            w[0] = w[1], w[1] = f;
+            f = w[2], w[2] = w[3], w[3] = f;
+          }
+          if (rot & TWO) {
+            const uint32_t f = w[0], g = w[1];
+            w[0] = w[2], w[1] = w[3], w[2] = f, w[3] = g;
           }
 #pragma unroll
           for (int e = 0; e < NE; ++e) {
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
             if constexpr (BITS == 8) l = levels8<8>(w[2 * e], w[2 * e + 1]);
             else if constexpr (BITS == 4) l = levels8<4>(w[e], 0u);
             else l = levels8<2>(w[e / 2] >> (16 * (e & 1)), 0u);
-            *reinterpret_cast<uint4 *>(z + z_at(t, NE * piece + ((e + rot) & (NE - 1)))) = l;
+            *reinterpret_cast<uint4 *>(z + (at ^ (uint32_t)(e << 4))) = l;
           }
         }
       } else {
@@ -462,22 +464,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       tc_fence_after();
       if (busy) {
         const uint32_t tp = tm + lanes + pl.col_p + wg * (kTile / 2);
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sig2 = make_float2(sig, sig), off2 = make_float2(-now, -now);
 #pragma unroll
         for (int c0 = 0; c0 < kTile / 2; c0 += 8) {
           uint32_t h[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * (c0 + c)]), sig, -now));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * (c0 + c) + 1]), sig, -now));
-            l4[(2 * c) & 3] += e0;
-            l4[(2 * c + 1) & 3] += e1;
-            const __half2 v = __floats2half2_rn(e0, e1);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * (c0 + c)]), __uint_as_float(s[2 * (c0 + c) + 1])),
+                                        sig2, off2);
+            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            l2[c & 1] = __fadd2_rn(l2[c & 1], e);
+            const __half2 v = __floats2half2_rn(e.x, e.y);
             h[c] = *reinterpret_cast<const uint32_t *>(&v);
           }
           tmem_st8(tp + c0, h);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         if (move) {
           // O holds every earlier tile once the last pooling is done
           const float f = raise ? exp2f(was - now) : 1.f;

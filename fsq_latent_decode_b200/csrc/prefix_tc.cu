@@ -23,15 +23,15 @@
 //
 // Q' is fp16, each row scaled by a power of two to its largest weight: 11
 // significant bits, finer than the bf16 of q and W_k it comes from.  P is fp16
-// with the running maximum at 2^6, so weights down to 2^-30 of it count.
+// too, in a window of its range (kTau).
 //
 // Q' lives in TMEM as the A operand: read from shared memory, both operands of
 // a score MMA would need more than its bandwidth.  TMEM columns: O [0, Gp), Q'
 // (Gp / 2), two P buffers of 32 (fp16), then as many 64-column S buffers as fit:
 // one at G = 256.  A softmax warp frees S as soon as it holds it in registers, so
-// the next scores run while this tile's exponentials do.  Shared memory is a ring of dequantised
-// tiles, deep enough that a tile waits in it from its scores to its pooling
-// while the next ones are made.
+// the next scores run while this tile's exponentials do.  Shared memory is a ring
+// of dequantised tiles, deep enough that a tile waits in it from its scores to its
+// pooling while the next ones are made.
 //
 // Warps (16): 0 copies, 1 and 2 issue the MMAs, 4-7 and 8-11 take the softmax of
 // every other tile (lane = query row) and 12-13 and 14-15 its dequantisation: a
@@ -43,6 +43,12 @@
 // parity tells only neighbouring phases apart.  (For the same reason S has two
 // buffers at most: S(i + 2) is announced after S(i) has been read.)
 // Every wait is bounded (FSQ_ERR_TIMEOUT), as in the other decode kernels.
+//
+// Measured: 95 us a call for 16 rows of 32 heads on 131072 shared tokens at G = 256
+// (69 GFLOP: 730 TFLOP/s, 44 % of the measured matrix rate), about 80 of them in
+// this kernel.  A tile keeps the tensor core busy for 1024 cycles and the four
+// schedulers for about 1300 (4.8k instructions: dequantisation, exponentials,
+// hand-offs); it takes about 1600.
 #include "common.cuh"
 #include "f16_codes.cuh"
 #include "query_f16.cuh"

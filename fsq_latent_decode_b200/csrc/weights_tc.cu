@@ -33,6 +33,11 @@
 // the scores, 12-19 (12-15 with many heads) dequantise.  A warp's way through a
 // tile is a chain of waits and loads, so two of each kind run side by side.
 // Every wait is bounded (FSQ_ERR_TIMEOUT).
+//
+// Measured: 197 us a call (graph replay; 216 us in a loop of calls) for 16 rows of
+// 131072 tokens at G = 256 and 32 heads (two passes over 268 MB: 2.7 TB/s).  A tile of 128 tokens takes about 1500
+// cycles: 3.1k (kAdd) to 3.8k (kLse) instructions on four schedulers and each
+// role's chain of waits; its codes' DRAM time would be 710.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>

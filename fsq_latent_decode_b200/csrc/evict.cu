@@ -23,6 +23,10 @@
 // ascending order from a counter, and a chunk publishes before it waits, so the
 // chunks waited for are always running or done: the wait ends whatever the
 // scheduling.  It is bounded all the same (FSQ_ERR_TIMEOUT).
+//
+// Measured, 16 rows of 131072 tokens cut to 65536, 128-byte rows: select 36 us,
+// compaction 57 us (277 MB: 4.9 TB/s); one row of 2048: 7.6 and 3 us.  The select
+// is a chain of about twenty barriers and dependent reads, not bandwidth.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -273,15 +277,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select(SelectParams p, in
     }
     kept += __shfl_sync(0xffffffffu, s, 31);
   };
-  each([&](int i, int64_t t, uint32_t k) {
+  auto keep_word = [&](int i, int64_t t, uint32_t k) {
     const bool same = need > 0 && t < N && k == limit;
     const uint32_t eq = __ballot_sync(0xffffffffu, same);
     const bool first = same && eq_before + __popc(eq & ((1u << lane) - 1u)) < ties;
     eq_before += __popc(eq);
     const uint32_t word = __ballot_sync(0xffffffffu, t < L && (t >= N || first || (need > 0 && k > limit)));
     if (lane == (i & 31)) mine = word;
-    if ((i & 31) == 31 || i == per - 1) flush(w0 + (i & ~31), (i & 31) + 1);
-  });
+    if (HELD == 0 && ((i & 31) == 31 || i == per - 1)) flush(w0 + (i & ~31), (i & 31) + 1);
+  };
+  each(keep_word);
+  if constexpr (HELD > 0) flush(w0, per);  // per <= 32; outside the unrolled loop, whose code has to fit its cache
   uint32_t sum;
   uint32_t base = block_prefix<NT>(lane == 0 ? kept : 0u, red, &sum);  // kept tokens of the warps before this one
   base = __shfl_sync(0xffffffffu, base, 0);

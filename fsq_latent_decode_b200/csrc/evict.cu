@@ -379,12 +379,12 @@ __global__ void __launch_bounds__(kCopyNT, 4) evict_compact(CopyParams p) {
     if (lane >= o) upto += v;
   }
   const int n = (int)__shfl_sync(0xffffffffu, upto, 31);
-  int rank[4];  // of this thread's tokens among the kept ones, -1: not kept
+  int rank[4] = {-1, -1, -1, -1};  // of this thread's tokens among the kept ones, -1: not kept
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    if (k * kCopyNT >= p.chunk) break;  // uniform
     const int t = tid + k * kCopyNT, w = t / 32;  // w < 32: the warp's word
     const uint32_t bits = __shfl_sync(0xffffffffu, word, w), to = __shfl_sync(0xffffffffu, upto, w);
-    rank[k] = -1;
     if (t < p.chunk && ((bits >> lane) & 1u)) {
       rank[k] = (int)(to - __popc(bits >> lane));
       list[rank[k]] = (uint16_t)t;
@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kCopyNT, 4) evict_compact(CopyParams p) {
     const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 2048 (kCopyBytes / 16)
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
+      if (k * kCopyNT >= n * ppr) break;  // uniform: no index arithmetic for rows that go
       const int i = tid + k * kCopyNT;
       const int r = (int)((uint32_t)i * inv >> 16);
       if (i < n * ppr) v[k] = *reinterpret_cast<const uint4 *>(src + (int64_t)list[r] * p.R + (i - r * ppr) * 16);
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kCopyNT, 4) evict_compact(CopyParams p) {
     const int ppr = p.R / 16;
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
+      if (k * kCopyNT >= n * ppr) break;
       const int i = tid + k * kCopyNT;
       if (i < n * ppr) *reinterpret_cast<uint4 *>(to + (int64_t)i * 16) = v[k];
     }

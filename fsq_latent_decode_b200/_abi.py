@@ -8,6 +8,7 @@ fails loudly; there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 import os
@@ -441,8 +442,20 @@ def _launch(what, stream, *tensors):
     if torch.cuda.current_device() != dev:
         raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {tensors[0].device}")
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{what}: the stream must be on the tensors' device, got {stream.device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream() without the Stream object
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Outputs and workspaces that a wrapper allocates belong to the stream that
+    the call runs on: their memory is not handed out again before its work ends."""
+    import torch
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _heads(t, what):
@@ -478,7 +491,8 @@ def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, ep
     if q.dtype is not bf16:
         raise ValueError("q must be torch.bfloat16")
     if q_out is None:
-        q_out = torch.empty((n_tok, n_q, d_h), dtype=bf16, device=q.device)
+        with _on(stream):
+            q_out = torch.empty((n_tok, n_q, d_h), dtype=bf16, device=q.device)
     elif q_out.dtype is not bf16 or q_out.shape != q.shape:
         raise ValueError("q_out must be torch.bfloat16 of q's shape")
     if k is not None:
@@ -487,7 +501,8 @@ def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, ep
             raise ValueError("k must be torch.bfloat16 [n_tok, n_k, d_h] of the same tokens as q")
         n_k = k.shape[1]
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=bf16, device=k.device)
+            with _on(stream):
+                k_out = torch.empty(k.shape, dtype=bf16, device=k.device)
         elif k_out.dtype is not bf16 or k_out.shape != k.shape:
             raise ValueError("k_out must be torch.bfloat16 of k's shape")
         ldko = _heads(k_out, "k_out")
@@ -555,11 +570,13 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
     stride = _cache_stride(codes, rb, B, T, "codes") if T > 0 else 0
     dtype = torch.float32 if opts.out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((B, n_q, d_h), dtype=dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty((B, n_q, d_h), dtype=dtype, device=q.device)
     elif out.shape != q.shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
     s = _launch("decode_attn_prefix", stream, q, prefix, codes, W_kv, out, lens)
-    ws = (workspace or Workspace(q.device)).get(prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
+    with _on(stream):
+        ws = (workspace or Workspace(q.device)).get(prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
     st = decode_attn_prefix_raw(q.data_ptr(), B, n_q, d_h, prefix.data_ptr(), T_prefix, _opt_ptr(codes), stride, T, G,
                                 W_kv.data_ptr(), n_kv, opts, ws.data_ptr(), ws.numel(), out.data_ptr(), s)
     _check(st, "fsq_decode_attn_prefix")
@@ -574,7 +591,8 @@ def attn_weights(q, codes, W_kv, acc, T, n_kv, G, opts=None, workspace=None, str
     B, n_q, d_h = q.shape
     cs, as_ = _cache_stride(codes, rb, B, T, "codes"), _acc_stride(acc, B, T, "acc")
     s = _launch("attn_weights", stream, q, codes, W_kv, acc, lens)
-    ws = (workspace or Workspace(q.device)).get(attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
+    with _on(stream):
+        ws = (workspace or Workspace(q.device)).get(attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
     st = attn_weights_raw(q.data_ptr(), B, n_q, d_h, codes.data_ptr(), cs, T, G, W_kv.data_ptr(), n_kv, opts,
                           acc.data_ptr(), as_, ws.data_ptr(), ws.numel(), s)
     _check(st, "fsq_attn_weights")
@@ -606,7 +624,8 @@ def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=No
     nbytes = cache_evict_workspace_size(B, T, G, levels)
     if nbytes == 0:
         raise FsqError(FSQ_ERR_INVALID_ARG, "fsq_cache_evict_workspace_size")
-    ws = (workspace or Workspace(codes.device)).get(nbytes)
+    with _on(stream):
+        ws = (workspace or Workspace(codes.device)).get(nbytes)
     st = _lib().fsq_cache_evict(codes.data_ptr(), cs, acc.data_ptr(), as_, _opt_ptr(seq_lens), B, T, n_keep, n_recent, G,
                                 levels, out.data_ptr(), os_, acc_out.data_ptr(), aos, _opt_ptr(lens_out),
                                 _opt_ptr(kept), ws.data_ptr(), ws.numel(), s)

@@ -437,3 +437,32 @@ def test_serving_run():
     want = np.concatenate([O.decode_attn(dq[b:b + 1].float().cpu().numpy(), rows[b][None], W.float().numpy(), n_kv, G,
                                          rope_knorm=rk) for b in range(B)])
     assert rel_err(got.cpu().numpy(), want) <= TOL
+
+
+def test_results_on_a_given_stream_outlive_later_allocations():
+    """stream=: what a wrapper allocates belongs to that stream, so tensors made
+    meanwhile on the current one do not land in a workspace that is in use."""
+    B, n_q, n_kv, G, Tp, T = 2, 16, 8, 256, 300, 100
+    prefix, codes, W, q = _case(B, n_q, n_kv, G, 16, Tp, T, 5)
+    dq, dp, dc, dW = _dev(q), _dev(prefix), _dev(codes), _dev(W)
+    acc = torch.zeros((B, T), device=DEV)
+
+    def calls(stream):
+        x = F.qk_norm_rope(dq, stream=stream)
+        o = F.decode_attn_prefix(x, dp, dc, dW, Tp, T, n_kv, G, stream=stream)
+        a = F.attn_weights(x, dc, dW, acc, T, n_kv, G, stream=stream)
+        return x, o, a
+
+    want = [t.clone() for t in calls(None)]
+    acc.zero_()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # about 10 ms: the calls queue behind it
+    got = calls(s)
+    fill = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in (256, 2048, 8192, 65536, 1 << 18, 1 << 20, 4 << 20)
+            for _ in range(4)]
+    s.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    del fill

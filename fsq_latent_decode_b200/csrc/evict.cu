@@ -24,8 +24,8 @@
 // chunks waited for are always running or done: the wait ends whatever the
 // scheduling.  It is bounded all the same (FSQ_ERR_TIMEOUT).
 //
-// Measured, 16 rows of 131072 tokens cut to 65536, 128-byte rows: select 36 us,
-// compaction 57 us (277 MB: 4.9 TB/s); one row of 2048: 7.6 and 3 us.  The select
+// Measured, 16 rows of 131072 tokens cut to 65536, 128-byte rows: select 34 us,
+// compaction 56 us (277 MB: 5.0 TB/s); one row of 2048: 7.2 and 2.9 us.  The select
 // is a chain of about twenty barriers and dependent reads, not bandwidth.
 #include <cooperative_groups.h>
 

@@ -54,6 +54,7 @@ bool prefix_supported(int n_q, int G);
 int prefix_rows_per_tile(int n_q);
 int prefix_max_splits();
 int prefix_tile_tokens();
+int prefix_split_tiles();
 size_t prefix_query_bytes(int G);
 cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, const uint8_t *shared, int64_t Tp,
                           const uint8_t *codes, int64_t bstride, int64_t T, const int32_t *seq_lens, int G, int bits,
@@ -276,6 +277,8 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
       if (kk == 1) break;
     }
   }
+  // fp16 weights hold a split's tail up to this length
+  if (k > prefix_split_tiles()) k = prefix_split_tiles();
   // a row's partials fit the merge
   while ((nt + k - 1) / k + (no + k - 1) / k > prefix_max_splits()) k *= 2;
   const int64_t Sp = (nt + k - 1) / k, Ss = (no + k - 1) / k;

@@ -69,12 +69,18 @@ constexpr int kMaxStages = 6, kMaxZ = 6, kMaxS = 2;
 constexpr int kDqWarps = 2;                        // of a group; the two groups take turns
 constexpr int kMiscBytes = 2048;
 constexpr size_t kSmemMax = 227 * 1024;
-// A row's reference m, its first tile's maximum, enters P as 2^0 and moves when a
-// score exceeds it by 2^kTau, so P stays below 2^15 (fp16 ends at 2^16) and
-// weights count down to 2^-24 of the reference.  Scores climb some powers of two
-// beyond a tile's first maximum, and moving O holds the whole CTA up for longer
-// than a tile takes, so the window is as wide as fp16 lets it be.
+// P is fp16: a row's weights are 2^(s - m), its reference m moves when a score
+// exceeds it by kTau, so P stays below 2^15 (fp16 ends at 2^16), and m is set
+// `lift` below the maximum of the tile that sets it.  Of n tokens of a split none
+// loses more than 2^-25 - lift of the largest weight to fp16's smallest step, all
+// together n 2^-25 - lift: lift is the smallest that keeps this at 2^-13, 0 up to
+// 4096 tokens.  (The sum l takes the rounded weights, so that what rounding does
+// to a weight, it does above and below the fraction bar.)  Scores climb some powers
+// of two beyond a tile's first maximum, and moving O holds the whole CTA up for
+// longer than a tile takes, so the window above is as wide as the tail lets it be.
 constexpr float kTau = 15.f;
+constexpr int kTailBits = 12, kMaxLift = 10;
+static_assert(kTile == 1 << 6, "prefix_split_tiles counts tiles of 64 tokens");
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 1000000000ull;
 
@@ -116,6 +122,7 @@ struct Params {
   uint32_t *err;
   int B, n_q, G, rpt;       // rpt: batch rows per query tile
   int QT, Sp, Ss, k;        // query tiles, splits of the prefix and of a row's own tokens, tiles per split
+  float lift;               // of a split's first maximum above the reference
   uint32_t stall_ns;
 };
 
@@ -129,6 +136,13 @@ struct Misc {
   float m[kRows];                          // the rows' references
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
+
+// (x, y) += v, in fp32
+__device__ __forceinline__ void add_f16x2(float2 &a, __half2 v) {
+  asm("{\n\t.reg .f16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.f16 %0, x, %0;\n\tadd.rn.f32.f16 %1, y, %1;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+}
 
 // 16-byte chunk c (8 coordinates) of token row t in the swizzled atoms
 __device__ __forceinline__ uint32_t z_at(int t, int c) {
@@ -457,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       if (i > 0) ok = warp_wait(&ms.decided[wg ^ 1][q4], (uint32_t)((i - 1) >> 1) & 1u, abort, kWaitNs) && ok;
       const float was = *(volatile float *)&ms.m[r];
       const bool raise = live && (top > was + kTau || (i == 0 && top > was));
-      const float now = raise ? top : was;
+      const float now = raise ? top - p.lift : was;
       if (raise) *(volatile float *)&ms.m[r] = now;
       const bool move = __any_sync(0xffffffffu, raise) && i > 0;
       __syncwarp();
@@ -479,9 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
           for (int c = 0; c < 8; ++c) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * (c0 + c)]), __uint_as_float(s[2 * (c0 + c) + 1])),
                                         sig2, off2);
-            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            l2[c & 1] = __fadd2_rn(l2[c & 1], e);
-            const __half2 v = __floats2half2_rn(e.x, e.y);
+            const __half2 v = __floats2half2_rn(ex2_approx(x.x), ex2_approx(x.y));
+            add_f16x2(l2[c & 1], v);
             h[c] = *reinterpret_cast<const uint32_t *>(&v);
           }
           tmem_st8(tp + c0, h);
@@ -781,6 +794,7 @@ bool prefix_supported(int n_q, int G) { return n_q <= tc::prefix::kRows && G <= 
 int prefix_rows_per_tile(int n_q) { return tc::prefix::kRows / n_q; }
 int prefix_max_splits() { return tc::prefix::kMaxSplits; }
 int prefix_tile_tokens() { return tc::prefix::kTile; }
+int prefix_split_tiles() { return 1 << (tc::prefix::kTailBits + tc::prefix::kMaxLift - 6); }
 size_t prefix_query_bytes(int G) {  // Q' of one query head
   return (size_t)((G + tc::prefix::kAtom - 1) / tc::prefix::kAtom) * tc::prefix::kAtom * 2;
 }
@@ -790,8 +804,10 @@ cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, const
                           const uint16_t *W_kv, float scale, int QT, int Sp, int Ss, int k, uint8_t *qbuf, float *sig,
                           float *part, uint32_t *err, void *o, int out_fp32, uint32_t stall_ns,
                           void *const *prof, cudaStream_t st) {
+  int lift = 0;
+  while (lift < tc::prefix::kMaxLift && (int64_t)k * tc::prefix::kTile > (int64_t)1 << (tc::prefix::kTailBits + lift)) ++lift;
   tc::prefix::Params p{shared, codes, bstride, Tp, T, seq_lens, qbuf, sig, part, err,
-                       (int)B, n_q, G, prefix_rows_per_tile(n_q), QT, Sp, Ss, k, stall_ns};
+                       (int)B, n_q, G, prefix_rows_per_tile(n_q), QT, Sp, Ss, k, (float)lift, stall_ns};
   return bits == 2   ? tc::prefix::launch_t<2>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st)
          : bits == 4 ? tc::prefix::launch_t<4>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st)
                      : tc::prefix::launch_t<8>(q, W_kv, n_kv, scale, p, qbuf, sig, o, out_fp32, prof, st);

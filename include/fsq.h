@@ -292,8 +292,11 @@ FSQ_API const char *fsq_decode_attn_kernel(int64_t B, int n_new, int64_t T, int 
  *  q, W_kv, o, opts, workspace (fsq_decode_attn_prefix_workspace_size): as in
  *  fsq_decode_attn, except that q is read after the kernels before it; the
  *  form is the absorbed one (variant AUTO or ABSORBED, rope_knorm 0; others
- *  return FSQ_ERR_UNSUPPORTED).  opts->num_splits counts splits of the prefix.
- * Q' = W_k^T q is held in fp16, scaled per head (11 significant bits).
+ *  return FSQ_ERR_UNSUPPORTED).  opts->num_splits counts splits of the prefix, of
+ *  2^22 tokens at most each.
+ * Q' = W_k^T q is held in fp16, scaled per head (11 significant bits).  The
+ * softmax weights are fp16 in the pooling and in their sum; those too small for
+ * it are off by 2^-13 of a split's largest weight in all, at most.
  * Needs: d_h == 128, n_q % n_kv == 0, n_q <= 128, G <= 256 and the G rules of
  * the append, T_prefix >= 1, T >= 0, B <= 65535.  B == 0 is a no-op. */
 FSQ_API size_t fsq_decode_attn_prefix_workspace_size(int64_t B, int64_t T_prefix, int64_t T, int n_q, int n_kv,

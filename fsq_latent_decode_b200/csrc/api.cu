@@ -290,7 +290,7 @@ fsq_status plan_prefix(int64_t B, int64_t Tp, int64_t T, int n_q, int n_kv, int 
   p->k = (int)k;
   size_t off = kWsHeader;
   p->off_q = off;
-  off = align_up(off + prefix_query_bytes(G) * (size_t)Bc * n_q, 256);
+  off = align_up(off + prefix_query_bytes(G) * (size_t)QT, 256);
   p->off_sig = off;
   off = align_up(off + sizeof(float) * (size_t)Bc * n_q, 256);
   p->off_part = off;

@@ -81,6 +81,19 @@ __device__ __forceinline__ void mma_ts_warp(uint32_t el, uint32_t d, uint32_t a,
       "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSwzHi), "r"(el)
       : "memory");
 }
+// D[tmem] (+)= A[smem] B[smem], both operands K-major atoms; issued alike.
+__device__ __forceinline__ void mma_ss_warp(uint32_t el, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSwzHi), "r"(el)
+      : "memory");
+}
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t m, uint32_t a) {
   const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m),

@@ -21,17 +21,20 @@
 // not drift one way.  Pairs come out as codes k and k + 4 of a group of eight;
 // Q' and the result use that order.
 //
-// Q' is fp16, each row scaled by a power of two to its largest weight: 11
-// significant bits, finer than the bf16 of q and W_k it comes from.  P is fp16
-// too, in a window of its range (kTau).
+// Q' is two fp16 terms, hi and lo (22 significant bits: the scores keep fp32's
+// precision, also where they spread over hundreds of powers of two), each row
+// scaled by a power of two to its largest weight.  The lo products go into S first,
+// while its sums are small.  P is fp16, in a window of its range (kTau).
 //
 // Q' lives in TMEM as the A operand: read from shared memory, both operands of
-// a score MMA would need more than its bandwidth.  TMEM columns: O [0, Gp), Q'
-// (Gp / 2), two P buffers of 32 (fp16), then as many 64-column S buffers as fit:
-// one at G = 256.  A softmax warp frees S as soon as it holds it in registers, so
-// the next scores run while this tile's exponentials do.  Shared memory is a ring
-// of dequantised tiles, deep enough that a tile waits in it from its scores to its
-// pooling while the next ones are made.
+// a score MMA need more than its bandwidth (48 cycles instead of 32).  TMEM
+// columns: O [0, Gp), Q' hi (Gp / 2), Q' lo (Gp / 2), two P buffers of 32 (fp16),
+// then as many 64-column S buffers as fit.  From Gp = 208 on they do not: there lo
+// stays in shared memory after all, and the ring gives up two of its six tiles.  A
+// softmax warp frees S as soon as it holds it in registers, so the next scores run
+// while this tile's exponentials do.  Shared memory is a ring of dequantised tiles,
+// deep enough that a tile waits in it from its scores to its pooling while the next
+// ones are made.
 //
 // Warps (16): 0 copies, 1 and 2 issue the MMAs, 4-7 and 8-11 take the softmax of
 // every other tile (lane = query row) and 12-13 and 14-15 its dequantisation: a
@@ -44,11 +47,11 @@
 // buffers at most: S(i + 2) is announced after S(i) has been read.)
 // Every wait is bounded (FSQ_ERR_TIMEOUT), as in the other decode kernels.
 //
-// Measured: 95 us a call for 16 rows of 32 heads on 131072 shared tokens at G = 256
-// (69 GFLOP: 730 TFLOP/s, 44 % of the measured matrix rate), about 80 of them in
-// this kernel.  A tile keeps the tensor core busy for 1024 cycles and the four
-// schedulers for about 1300 (4.8k instructions: dequantisation, exponentials,
-// hand-offs); it takes about 1600.
+// Measured: 107 us a call for 16 rows of 32 heads on 131072 shared tokens at G = 256
+// (69 GFLOP: 645 TFLOP/s, 39 % of the measured matrix rate; with the lo products
+// 102 GFLOP), about 90 of them in this kernel; with hi alone, 96.  A tile keeps the
+// tensor core busy for 1792 cycles (lo 768, hi 512, pooling 512); the four schedulers
+// need about 1300 (4.8k instructions: dequantisation, exponentials, hand-offs).
 #include "common.cuh"
 #include "f16_codes.cuh"
 #include "query_f16.cuh"
@@ -64,7 +67,10 @@ constexpr int kTile = 64;                          // tokens of a tile
 constexpr int kThreads = 512;                      // 128 registers a thread: a softmax thread holds 64 scores
 constexpr int kAtom = 64;                          // coordinates of a swizzled atom row (128 bytes)
 constexpr int kAtomBytes = kTile * 128;            // 64 coordinates of a tile
-constexpr int kMaxG = 256;                         // O, Q', two P and one S buffer fill TMEM
+constexpr int kMaxG = 256;                         // O, Q' hi, two P and one S buffer fill TMEM
+constexpr int kLoTmem = 192;                       // widest Gp whose Q' lo fits beside them
+constexpr int kQAtomBytes = kRows * 128;           // 64 coordinates of Q' lo in shared memory
+constexpr int kTop = 12;                           // Q' is scaled to a largest weight of 2^12 .. 2^13: its lo terms stay normal
 constexpr int kMaxStages = 6, kMaxZ = 6, kMaxS = 2;
 constexpr int kDqWarps = 2;                        // of a group; the two groups take turns
 constexpr int kMiscBytes = 2048;
@@ -87,16 +93,18 @@ constexpr uint64_t kDrainNs = 1000000000ull;
 // Shared-memory and TMEM plan of a CTA.
 struct Plan {
   int Gp, NA, R, stages, nz, ns;
-  uint32_t z_bytes, stage_bytes, off_c, off_misc, total, col_q, col_p, col_s;
+  uint32_t z_bytes, stage_bytes, off_l, off_c, off_misc, total, col_q, col_l, col_p, col_s;
 };
 __host__ __device__ inline Plan plan_of(int G, int bits) {
   Plan p;
   p.Gp = (G + 15) / 16 * 16;
   p.NA = (G + kAtom - 1) / kAtom;
   p.R = G * bits / 8;
-  p.nz = kMaxZ;
+  const bool tmem = p.Gp <= kLoTmem;  // Q' lo
+  p.nz = tmem ? kMaxZ : kMaxZ - 2;
   p.z_bytes = (uint32_t)(p.NA * kAtomBytes);
-  p.off_c = p.nz * p.z_bytes;
+  p.off_l = p.nz * p.z_bytes;
+  p.off_c = p.off_l + (tmem ? 0 : p.NA * kQAtomBytes);
   // +16: the last token's last group may read past its row
   p.stage_bytes = (uint32_t)(kTile * p.R + 16 + 127) / 128 * 128;
   p.stages = (int)((kSmemMax - kMiscBytes - p.off_c) / p.stage_bytes);
@@ -104,7 +112,8 @@ __host__ __device__ inline Plan plan_of(int G, int bits) {
   p.off_misc = p.off_c + p.stages * p.stage_bytes;
   p.total = p.off_misc + kMiscBytes;
   p.col_q = p.Gp;
-  p.col_p = p.col_q + p.Gp / 2;
+  p.col_l = p.col_q + p.Gp / 2;
+  p.col_p = p.col_l + (tmem ? p.Gp / 2 : 0);
   p.col_s = p.col_p + 2 * (kTile / 2);
   p.ns = (int)(512 - p.col_s) / kTile;
   if (p.ns > kMaxS) p.ns = kMaxS;
@@ -116,7 +125,10 @@ struct Params {
   const uint8_t *codes;     // own rows
   int64_t bstride, Tp, T;
   const int32_t *seq_lens;
-  const uint8_t *qbuf;      // Q', fp16 [B n_q][NA 64], physical order
+  // Q', fp16 [QT][hi, lo], physical order: [8 NA chunks of 8][128 rows], so that a
+  // warp reads a chunk of its rows at once; lo in swizzled atoms where it stays in
+  // shared memory
+  const uint8_t *qbuf;
   const float *sig;         // [B n_q] score scales
   float *part;              // [B][S][n_q][2 + G]
   uint32_t *err;
@@ -130,7 +142,7 @@ struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t z_ready[kMaxZ], z_free[kMaxZ];  // z_free: the tile's pooling is done
   uint64_t s_full[2], s_free[kMaxS], p_ready[2];  // s_full, p_ready: even and odd tiles
-  uint64_t q_ready, done[2], never;
+  uint64_t q_ready, l_full, done[2], never;
   uint32_t tmem_base, abort;
   uint64_t decided[2][4];                  // per softmax warp: the tile's reference stands
   float m[kRows];                          // the rows' references
@@ -213,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     }
     for (int i = 0; i < 8; ++i) mbar_init(&ms.decided[i / 4][i % 4], 1);
     mbar_init(&ms.q_ready, 8);
+    mbar_init(&ms.l_full, 1);
     mbar_init(&ms.done[0], 1);
     mbar_init(&ms.done[1], 1);
     mbar_init(&ms.never, 1);  // completed by nothing: the test-only stall waits on it
@@ -238,6 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     // ------------------------------------------------------------ producer
     pdl_wait();  // for the query prologue, which waited for whatever wrote the codes
     if (bad_len && split == 0 && lane == 0) record_error(p.err, FSQ_ERR_INVALID_ARG);
+    // Q' lo, of the whole tile: what rows without a query get, they alone see
+    if (Gp > kLoTmem && lane == 0) {
+      mbar_arrive_expect_tx(&ms.l_full, NA * kQAtomBytes);
+      bulk_g2s(smem + pl.off_l, p.qbuf + (int64_t)(2 * qt + 1) * (NA * kQAtomBytes), NA * kQAtomBytes, &ms.l_full);
+    }
     // a row's own tokens are read once; the tiles of the prefix by every query tile
     const uint64_t pol = own ? l2_evict_first() : l2_evict_normal();
     bool ok = true;
@@ -271,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
       if (lane == 0) fail();
       for (int i = max(0, issued - stages); i < issued; ++i)
         drain_bar(&ms.full[i % stages], (uint32_t)(i / stages) & 1u, kDrainNs);
+      if (Gp > kLoTmem) drain_bar(&ms.l_full, 0, kDrainNs);
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers (whole warps, one lane issues):
@@ -283,18 +302,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     const uint32_t id_o = idesc_f16(kRows, Gp, 0, 1), el = elect_one();
     bool ok = true;
     if (warp == 1) {
-      ok = warp_wait(&ms.q_ready, 0, abort, kWaitNs);
+      ok = warp_wait(&ms.q_ready, 0, abort, kWaitNs) && (Gp <= kLoTmem || warp_wait(&ms.l_full, 0, abort, kWaitNs));
       with_count<1, kMaxG / 16>(Gp / 16, [&](auto ks) {
+      constexpr bool LO_SMEM = 16 * decltype(ks)::value > kLoTmem;
+      const uint32_t lo_s = swz_lo(z_a + pl.off_l, 16);
       Ring z, s;
       for (int i = 0; ok && i < n_tiles; ++i, z.next(nz), s.next(ns)) {
         ok = warp_wait(&ms.s_free[s.slot], s.par ^ 1u, &ms.z_ready[z.slot], z.par, abort, kWaitNs);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tm + pl.col_s + s.slot * kTile, a = tm + pl.col_q;
+        const uint32_t d = tm + pl.col_s + s.slot * kTile, a = tm + pl.col_q, lo = tm + pl.col_l;
         const uint32_t b = swz_lo(z_a + z.slot * pl.z_bytes, 16);
 #pragma unroll
+        for (int k = 0; k < decltype(ks)::value; ++k) {
+          const uint32_t bk = b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4);
+          if constexpr (LO_SMEM)
+            mma_ss_warp(el, d, lo_s + (((k >> 2) * kQAtomBytes + (k & 3) * 32) >> 4), bk, id_s, k > 0 ? 1u : 0u);
+          else mma_ts_warp(el, d, lo + 8 * k, bk, id_s, k > 0 ? 1u : 0u);
+        }
+#pragma unroll
         for (int k = 0; k < decltype(ks)::value; ++k)
-          mma_ts_warp(el, d, a + 8 * k, b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+          mma_ts_warp(el, d, a + 8 * k, b + (((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4), id_s, 1u);
         if (el) tc_commit(&ms.s_full[i & 1]);
         __syncwarp();
       }
@@ -409,18 +437,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
     pdl_wait();  // Q' and sig come from the query prologue
     float sig = 0.f;
     {
-      // half of the row's Q' into TMEM; rows without a query are zero
-      const uint8_t *qr = p.qbuf + ((int64_t)qt * p.rpt * p.n_q + r) * (NA * 128);
+      // half of the row's Q' into TMEM, lo as far as it fits; rows without a query are zero
+      const uint8_t *qr = p.qbuf + (int64_t)qt * (2 * NA * kQAtomBytes) + r * 16;
       if (live) sig = p.sig[(int64_t)qt * p.rpt * p.n_q + r];
+#pragma unroll 1
+      for (int term = 0; term < (Gp > kLoTmem ? 1 : 2); ++term, qr += NA * kQAtomBytes) {
 #pragma unroll 4
-      for (int c = 8 * wg; c < Gp / 2; c += 16) {  // columns: two coordinates each
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (live) {
-          a = *reinterpret_cast<const uint4 *>(qr + 4 * c);
-          b = *reinterpret_cast<const uint4 *>(qr + 4 * c + 16);
+        for (int c = 8 * wg; c < Gp / 2; c += 16) {  // columns: two coordinates each
+          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+          if (live) {
+            a = *reinterpret_cast<const uint4 *>(qr + (c >> 2) * (16 * kRows));
+            b = *reinterpret_cast<const uint4 *>(qr + ((c >> 2) + 1) * (16 * kRows));
+          }
+          const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          tmem_st8(tm + lanes + (term ? pl.col_l : pl.col_q) + c, v);
         }
-        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        tmem_st8(tm + lanes + pl.col_q + c, v);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -584,25 +615,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_split_tc(Params p) {
 // ---------------------------------------------------------------- prologue
 // Per (kv head j, batch row b): q'_h[g] = c sum_d W_k[j d_h + d][g] q_h[d] (c =
 // scale log2 e), scaled by the power of two that brings the head's largest
-// weight into [1, 2), as a row of fp16 in physical order; sig_h takes the power
-// back.  Also clears the error word.
+// weight into [2^kTop, 2^(kTop + 1)), as two rows of fp16, hi and lo, in physical
+// order of their tile's chunks; sig_h takes the power back.  Also clears the error word.
 template <int BITS>
 __global__ void __launch_bounds__(kAbsorbThreads, 1) prefix_query(const uint16_t *__restrict__ q,
                                                                const uint16_t *__restrict__ W_kv, int n_q, int n_kv,
-                                                               int G, int NA, float c, uint8_t *__restrict__ qbuf,
+                                                               int G, int NA, int rpt, float c, uint8_t *__restrict__ qbuf,
                                                                float *__restrict__ sig, uint32_t *err) {
   __shared__ AbsorbSmem<kMaxG> sm;
   const int64_t b = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *err = 0u;
+  uint8_t *tile = qbuf + b / rpt * (2 * NA * kQAtomBytes);
+  const int r0 = (int)(b % rpt) * n_q;
+  const bool atoms = (G + 15) / 16 * 16 > kLoTmem;  // of lo
   absorb_heads(
       sm, q, W_kv, n_q, n_kv, G, NA * kAtom, c, blockIdx.x, b,
       [&](int h, int g, float v, int e) {
-        reinterpret_cast<__half *>(qbuf)[(b * n_q + h) * (NA * kAtom) + ((g & ~7) | order_of<BITS>(g & 7))] =
-            __float2half_rn(scalbnf(v, -e));
+        const int r = r0 + h, ch = g >> 3, x = 2 * order_of<BITS>(g & 7);
+        const float s = scalbnf(v, kTop - e);
+        const __half hi = __float2half_rn(s);
+        const int at = (ch * kRows + r) * 16 + x;
+        *reinterpret_cast<__half *>(tile + at) = hi;
+        *reinterpret_cast<__half *>(tile + NA * kQAtomBytes + (atoms ? (ch >> 3) * kQAtomBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4) + x : at)) =
+            __float2half_rn(s - __half2float(hi));
       },
-      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e); });
+      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop); });
 }
 
 // ---------------------------------------------------------------- split merge
@@ -768,7 +807,7 @@ cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float sc
                      float *sig, void *o, int out_fp32, void *const *prof, cudaStream_t st) {
   const Plan pl = plan_of(p.G, BITS);
   cudaError_t e = launch_pdl(prefix_query<BITS>, dim3(n_kv, (unsigned)p.B), dim3(kAbsorbThreads), 0, st, q, W_kv, p.n_q, n_kv,
-                             p.G, pl.NA, scale * kLog2e, qbuf, sig, p.err);
+                             p.G, pl.NA, p.rpt, scale * kLog2e, qbuf, sig, p.err);
   if (e != cudaSuccess) return e;
   // one CTA per SM: each takes all of TMEM
   const size_t smem = pl.total > 120 * 1024 ? pl.total : 120 * 1024;
@@ -795,8 +834,8 @@ int prefix_rows_per_tile(int n_q) { return tc::prefix::kRows / n_q; }
 int prefix_max_splits() { return tc::prefix::kMaxSplits; }
 int prefix_tile_tokens() { return tc::prefix::kTile; }
 int prefix_split_tiles() { return 1 << (tc::prefix::kTailBits + tc::prefix::kMaxLift - 6); }
-size_t prefix_query_bytes(int G) {  // Q' of one query head
-  return (size_t)((G + tc::prefix::kAtom - 1) / tc::prefix::kAtom) * tc::prefix::kAtom * 2;
+size_t prefix_query_bytes(int G) {  // Q' of a query tile, hi and lo
+  return (size_t)((G + tc::prefix::kAtom - 1) / tc::prefix::kAtom) * tc::prefix::kQAtomBytes * 2;
 }
 
 cudaError_t launch_prefix(const uint16_t *q, int64_t B, int n_q, int n_kv, const uint8_t *shared, int64_t Tp,

@@ -294,7 +294,7 @@ FSQ_API const char *fsq_decode_attn_kernel(int64_t B, int n_new, int64_t T, int 
  *  form is the absorbed one (variant AUTO or ABSORBED, rope_knorm 0; others
  *  return FSQ_ERR_UNSUPPORTED).  opts->num_splits counts splits of the prefix, of
  *  2^22 tokens at most each.
- * Q' = W_k^T q is held in fp16, scaled per head (11 significant bits).  The
+ * Q' = W_k^T q is held as two fp16 terms (22 significant bits); the
  * softmax weights are fp16 in the pooling and in their sum; those too small for
  * it are off by 2^-13 of a split's largest weight in all, at most.
  * Needs: d_h == 128, n_q % n_kv == 0, n_q <= 128, G <= 256 and the G rules of

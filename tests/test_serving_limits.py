@@ -9,7 +9,7 @@ import torch
 import fsq_latent_decode_b200 as F
 from oracle import fsq_oracle as O
 
-from cases import decoder_weights
+from cases import decoder_weights, oracle_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,41 @@ def test_prefix_counts_a_long_tail(splits):
     eps = (2.0 ** -13 + t * math.log(2) * 2.0 ** -20 * size) * apart + \
         N / 16 * 2.0 ** -23 * (np.abs(strong) + t * np.abs(tail)) + N / 64 * 2.0 ** -24 * np.abs(want).max()
     assert (np.abs(got[0].double().cpu().numpy() - want) <= np.abs(Wv) @ eps + 2.0 ** -20 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("G,L", [(256, 16), (84, 16), (80, 256), (256, 256), (256, 4), (192, 16), (208, 16), (240, 256)])
+@pytest.mark.parametrize("q_scale", [1.0, 8.0, 30.0])
+def test_prefix_holds_sharp_scores(q_scale, G, L):
+    """Scores that spread over hundreds of powers of two, in fp32 outputs, to the
+    roundings that are left: the weights' fp16 (half a step, 2^-11) and flush
+    (2^-25 of the largest, each), and the scores' fp32.
+
+    A score s in log2 units is a sum of Gp / 16 steps of the tensor core, each
+    truncating the products and the sum to 2^-23 of the largest partial sum M; its
+    queries carry 22 bits and fp32 sums, independent over the coordinates: 2^-20 M
+    is over four times their spread.  An output moves by the weights' relative
+    errors times sum_t p_t |v_t - o|."""
+    B, n_q, n_kv, Tp, T = 2, 16, 4, 1500, 40
+    prefix = oracle_cache(1, Tp, G, 610 + G, levels=L)[0, :Tp]
+    codes = oracle_cache(B, T, G, 611 + G, levels=L)
+    W, q = decoder_weights(n_q, n_kv, G, B, 612, levels=L)
+    q = (q.float() * q_scale).to(torch.bfloat16)
+    ws = F.Workspace()
+    got = F.decode_attn_prefix(_dev(q), _dev(prefix), _dev(codes), _dev(W), Tp, T, n_kv, G,
+                               opts=F.attn_opts(levels=L, out_fp32=True), workspace=ws).double().cpu().numpy()
+    assert F.workspace_status(ws.buf) == F.FSQ_OK
+    Wk, Wv = O.split_wkv(W.float().numpy().astype(np.float64), n_kv, 128)
+    pad = -G % 16
+    for b in range(B):
+        z = O.unpack(np.concatenate([prefix, codes[b, :T]]), G, L).astype(np.float64)
+        for h in range(n_q):
+            j = h // (n_q // n_kv)
+            qa = Wk[j].T @ q[b, h].double().numpy() / math.sqrt(128)
+            p, v = O.softmax(z @ qa), z @ Wv[j].T
+            o = p @ v
+            steps = np.pad(z * qa * LOG2E, ((0, 0), (0, pad))).reshape(len(z), -1, 16).sum(-1)
+            M = np.abs(np.cumsum(steps, 1)).max()
+            rel = 2.0 ** -11 + math.log(2) * ((G + pad) / 16 * 2.0 ** -22 + 2.0 ** -20) * M
+            away = np.abs(v - o)
+            tol = rel * (p @ away) + len(z) * 2.0 ** -25 * away.max(0) + 2.0 ** -18 * (np.abs(o) + p @ np.abs(v))
+            assert (np.abs(got[b, h] - o) <= tol).all(), (b, h, (np.abs(got[b, h] - o) / tol).max())

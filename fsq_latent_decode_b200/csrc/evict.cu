@@ -149,6 +149,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select(SelectParams p, in
     if (CS > 1) cl.sync();
     else __syncthreads();
   };
+  // A CTA's shared memory may be touched by the others only once it runs, which the
+  // cluster's first barrier tells: arrived at here, waited for behind the loads
+  // below, before any remote access, whichever of them a row's length leads to.
+  if (CS > 1) cl.barrier_arrive();
   pdl_wait();
   const int64_t given = p.lens ? p.lens[b] : p.T;
   const int64_t L = given < 0 ? 0 : (given > p.T ? p.T : given);
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select(SelectParams p, in
       }
     }
   };
+  if (CS > 1) cl.barrier_wait();
   uint32_t limit = 0, ties = need, equal = need;  // key of the last one that stays; how many of the keys equal to it do, of how many
   if (need > 0) {
     int shift = 32;

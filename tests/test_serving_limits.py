@@ -95,3 +95,31 @@ def test_prefix_holds_sharp_scores(q_scale, G, L):
             away = np.abs(v - o)
             tol = rel * (p @ away) + len(z) * 2.0 ** -25 * away.max(0) + 2.0 ** -18 * (np.abs(o) + p @ np.abs(v))
             assert (np.abs(got[b, h] - o) <= tol).all(), (b, h, (np.abs(got[b, h] - o) / tol).max())
+
+
+# ---------------------------------------------------------------- eviction: rows that stay whole, in clusters
+@pytest.mark.parametrize("B,T", [(300, 5000), (300, 20001), (150, 70000)])
+@pytest.mark.parametrize("recent", ["some", "all"])
+def test_evict_of_rows_without_a_choice(B, T, recent):
+    """Rows of several CTAs that select nothing, because they are short enough or
+    because only recent tokens stay, in more clusters than run at once, between rows
+    that do select."""
+    G, keep = 4, T - 700
+    n_recent = keep if recent == "all" else 100
+    r = np.random.default_rng(T)
+    codes = r.integers(0, 256, (B, (T + 15) // 16 * 16, 2), dtype=np.uint8)
+    acc = r.exponential(size=(B, T)).astype(np.float32)
+    lens = np.array([(keep, keep - 333, T, T - 1, 5)[b % 5] for b in range(B)], np.int32)
+    dc, da, dl = _dev(codes), _dev(acc), _dev(lens)
+    out, ao = torch.zeros((B, (keep + 15) // 16 * 16, 2), dtype=torch.uint8, device=DEV), torch.zeros((B, keep), device=DEV)
+    kept, lo, ws = torch.zeros((B, keep), dtype=torch.int32, device=DEV), torch.zeros_like(dl), F.Workspace()
+    want = [O.evict(acc[b], lens[b], keep, n_recent) if recent == "some" and lens[b] > keep
+            else np.arange(max(0, lens[b] - keep), lens[b]) for b in range(B)]
+    for _ in range(3):
+        F.cache_evict(dc, da, T, keep, n_recent, G=G, seq_lens=dl, out=out, acc_out=ao, lens_out=lo, kept=kept, workspace=ws)
+        assert F.workspace_status(ws.buf) == F.FSQ_OK
+        got, gc, ga = kept.cpu().numpy(), out.cpu().numpy(), ao.cpu().numpy()
+        assert np.array_equal(lo.cpu().numpy(), np.minimum(lens, keep))
+        for b, at in enumerate(want):
+            assert np.array_equal(got[b, :len(at)], at) and (got[b, len(at):] == -1).all()
+            assert np.array_equal(gc[b, :len(at)], codes[b, at]) and np.array_equal(ga[b, :len(at)], acc[b, at])

@@ -79,8 +79,11 @@ struct MergeScratch {
 // Workspace header: the device error word lives in the first 4 bytes.
 constexpr size_t kWsHeader = 256;
 
+// A call's gravest status stays: FSQ_ERR_TIMEOUT, whose outputs are undefined, over
+// FSQ_ERR_INVALID_ARG, whose lengths were clamped, whichever was recorded first.
+static_assert(-FSQ_ERR_TIMEOUT > -FSQ_ERR_INVALID_ARG, "the error word holds the larger of the two");
 __device__ __forceinline__ void record_error(uint32_t *err, int status) {
-  atomicCAS(err, 0u, (uint32_t)(-status));
+  atomicMax(err, (uint32_t)(-status));
 }
 
 // Cached tokens of batch row b: T, or seq_lens[b] for a ragged batch, clamped

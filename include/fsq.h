@@ -378,6 +378,9 @@ FSQ_API fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, con
  *             -1 behind the last, or NULL                              — written
  *  workspace  >= fsq_cache_evict_workspace_size(...) bytes, 256-byte aligned; its
  *             error word is read with fsq_workspace_status
+ * In place, a part of a row waits until the parts that it moves onto are read.  The
+ * wait is bounded; if it gives up, the call records FSQ_ERR_TIMEOUT and leaves codes,
+ * acc, lens_out and kept undefined.
  * Needs: L in {4, 16, 256} (0 = 16) and the G rules of the append; 0 <= T <=
  * 2^31 - 1; 1 <= n_keep, 0 <= n_recent <= n_keep <= 2^31 - 1; strides that
  * hold their rows; codes, codes_out and their strides 16-byte aligned, acc,
@@ -430,7 +433,8 @@ FSQ_API fsq_status fsq_decode_attn_noalloc_status(fsq_stream_t stream);
  * last used by fsq_decode_attn (each decode call clears it first), or an
  * append path's fsq_encode_opts.status_word (workspace_bytes >= 4).  Blocking
  * copy: synchronises with `stream`.  Returns FSQ_OK or the recorded device
- * status (e.g. FSQ_ERR_TIMEOUT); clears nothing. */
+ * status; of several, FSQ_ERR_TIMEOUT (undefined outputs) stays over
+ * FSQ_ERR_INVALID_ARG (clamped lengths).  Clears nothing. */
 FSQ_API fsq_status fsq_workspace_status(const void *workspace, size_t workspace_bytes, fsq_stream_t stream);
 
 FSQ_API const char *fsq_status_string(fsq_status s);

@@ -21,6 +21,43 @@ def _dev(a):
     return (a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))).to(DEV)
 
 
+def _lens(*n):
+    return torch.tensor(n, dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------------------- a wait that gives up beside a length out of range
+def test_weights_that_time_out_beside_a_bad_length_add_nothing():
+    """A length outside its range is clamped and recorded before any wait can give
+    up; the time-out is reported all the same, and nothing is added."""
+    G, T = 256, 3000
+    codes = oracle_cache(2, T, G, 601)
+    W, q = decoder_weights(32, 8, G, 2, 602)
+    acc, ws = torch.full((2, T), 0.5, device=DEV), F.Workspace()
+    a = (_dev(q), _dev(codes), _dev(W), acc, T, 8, G)
+    F.attn_weights(*a, opts=F.attn_opts(seq_lens=_lens(T + 1, T), debug_stall_ns=2_000_000), workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_ERR_TIMEOUT
+    assert (acc == 0.5).all()
+    F.attn_weights(*a, opts=F.attn_opts(seq_lens=_lens(T + 1, T)), workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_ERR_INVALID_ARG
+    assert np.allclose((acc.double() - 0.5).sum(1).cpu().numpy(), 32, rtol=1e-3)  # 2^-25 of 0.5 a token at most: 1e-4 of 3000
+
+
+@pytest.mark.parametrize("call", ["prefix", "decode", "generic"])
+def test_attention_that_times_out_beside_a_bad_length_says_so(call):
+    L, G, T = (4, 320, 500) if call == "generic" else (16, 256, 500)
+    codes = oracle_cache(2, T, G, 603, levels=L)
+    W, q = decoder_weights(32, 8, G, 2, 604, levels=L)
+    ws, out = F.Workspace(), []
+    for stall in (2_000_000, 0):
+        o = F.attn_opts(seq_lens=_lens(T + 1, T), debug_stall_ns=stall, levels=L)
+        if call == "prefix":
+            F.decode_attn_prefix(_dev(q), _dev(codes[0, :T]), _dev(codes), _dev(W), T, T, 8, G, opts=o, workspace=ws)
+        else:
+            F.decode_attn(_dev(q), _dev(codes), _dev(W), T, 8, G, opts=o, workspace=ws)
+        out.append(F.workspace_status(ws.buf))
+    assert out == [F.FSQ_ERR_TIMEOUT, F.FSQ_ERR_INVALID_ARG]
+
+
 # ---------------------------------------------------------------- shared prefix: tails and sharp softmaxes
 @pytest.mark.parametrize("splits", [1, 2, 0])
 def test_prefix_counts_a_long_tail(splits):

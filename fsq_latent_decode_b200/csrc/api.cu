@@ -343,7 +343,7 @@ fsq_status plan_weights(int64_t B, int64_t T, int n_q, int n_kv, int d_h, int G,
   p->off_q = off;
   off = align_up(off + weights_query_bytes(n_q, G, bits) * (size_t)Bc, 256);
   p->off_sig = off;
-  off = align_up(off + sizeof(float) * (size_t)Bc * n_q, 256);
+  off = align_up(off + 2 * sizeof(float) * (size_t)Bc * n_q, 256);
   p->off_part = off;
   off = align_up(off + 2 * sizeof(float) * (size_t)Bc * p->S * n_q, 256);
   p->total = off;

@@ -6,6 +6,8 @@
 // quarters meet in shared memory, and four warps per head take the head's
 // largest weight, by whose power of two the caller scales.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace fsq {
@@ -24,7 +26,8 @@ struct AbsorbSmem {
 // store(h, g, v, e): head h (of the whole call), coordinate g, q' and the
 // exponent of the head's largest weight (0 for a head of zeros and for one that
 // is not finite, whose results are not finite either); for every g < Gs, 0 from
-// G on.  scale(h, e) once per head.  Every thread of the CTA calls this.
+// G on.  scale(h, e) once per head; if store returns a float, scale(h, e, sum) with
+// the head's sum of them.  Every thread of the CTA calls this.
 template <int MAXG, class Store, class Scale>
 __device__ __forceinline__ void absorb_heads(AbsorbSmem<MAXG> &sm, const uint16_t *__restrict__ q,
                                              const uint16_t *__restrict__ W_kv, int n_q, int n_kv, int G, int Gs,
@@ -83,15 +86,29 @@ __device__ __forceinline__ void absorb_heads(AbsorbSmem<MAXG> &sm, const uint16_
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) sm.top[h][w4] = top;
     __syncthreads();
+    top = fmaxf(fmaxf(sm.top[h][0], sm.top[h][1]), fmaxf(sm.top[h][2], sm.top[h][3]));
+    const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
+    constexpr bool SUM = !std::is_void<decltype(store(0, 0, 0.f, 0))>::value;
+    float sum = 0.f;
     if (h < nh) {
-      top = fmaxf(fmaxf(sm.top[h][0], sm.top[h][1]), fmaxf(sm.top[h][2], sm.top[h][3]));
-      const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int g = cp + 128 * i;
-        if (g < Gs) store(j * grp + h0 + h, g, v[i], e);
+        if (g < Gs) {
+          if constexpr (SUM) sum += store(j * grp + h0 + h, g, v[i], e);
+          else store(j * grp + h0 + h, g, v[i], e);
+        }
       }
-      if (cp == 0) scale(j * grp + h0 + h, e);
+    }
+    if constexpr (SUM) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncthreads();  // sm.top has been read
+      if (lane == 0) sm.top[h][w4] = sum;
+      __syncthreads();
+      if (h < nh && cp == 0) scale(j * grp + h0 + h, e, (sm.top[h][0] + sm.top[h][1]) + (sm.top[h][2] + sm.top[h][3]));
+    } else {
+      if (h < nh && cp == 0) scale(j * grp + h0 + h, e);
     }
     __syncthreads();
   }

@@ -9,13 +9,16 @@
 // kAdd goes through its tiles backwards: the last codes of the first pass are
 // still in L2.
 //
-// The result is a running fp32 sum over many steps, so scores are exact to fp32:
-// Q' = W_k^T q * scale * log2 e is held as two fp16 terms per head (22 bits),
-// scaled by a power of two, against the codes n themselves (4 and 8 bits): the
-// level offset -L/2 moves all of a head's scores alike, which the softmax does not
-// see.  A code stays where it lies in its word, as the mantissa of an fp16
-// subnormal (n 2^-24 times the power of two of its place, which Q' takes off): one
-// LOP3 per pair.
+// The result is a running fp32 sum over many steps, so scores keep an fp32 sum's
+// precision: Q' = W_k^T q * scale * log2 e is held as two fp16 terms per head (22
+// bits), scaled by a power of two.  2- and 8-bit codes enter as signed levels.  4-bit
+// codes enter as they lie in their word, as the mantissa of an fp16 subnormal (n 2^-24
+// times the power of two of its place, which Q' takes off): one LOP3 per pair, where
+// levels take two instructions (203 against 234 us in the case below).  Their offset
+// 8 sum_g q'_g, which can be hundreds of times a score where W_k has a component that
+// all coordinates share, may not cost precision: the hi term is an integer of 11
+// bits in units of a grid (10 above G = 512), so that S_hi, below 2^24 of them, is
+// exact, and 8 sum_g hi_g leaves it, exactly, before S_lo joins.
 //   S [128 tokens x 2 n_q] = Z [128 x G] . [Q'_hi ; Q'_lo]^T      score = S_hi + S_lo
 // A token is a TMEM lane, so a softmax thread owns its tokens: kLse keeps
 // (reference, sum) per head and thread, the first token's score as the
@@ -34,7 +37,7 @@
 // tile is a chain of waits and loads, so two of each kind run side by side.
 // Every wait is bounded (FSQ_ERR_TIMEOUT).
 //
-// Measured: 197 us a call (graph replay; 216 us in a loop of calls) for 16 rows of
+// Measured: 199-203 us a call (graph replay; 218 us in a loop of calls) for 16 rows of
 // 131072 tokens at G = 256 and 32 heads (two passes over 268 MB: 2.7 TB/s).  A tile of 128 tokens takes about 1500
 // cycles: 3.1k (kAdd) to 3.8k (kLse) instructions on four schedulers and each
 // role's chain of waits; its codes' DRAM time would be 710.
@@ -134,7 +137,7 @@ struct Params {
   int64_t bstride, T;
   const int32_t *seq_lens;
   const uint8_t *qbuf;   // per batch row: Q' in the score MMA's B layout
-  const float *sig;      // [B][n_q] score scales
+  const float2 *sig;     // [B][n_q] score scales, and the offset that S_hi sheds first (negated)
   float2 *part;          // [B][S][n_q] (max, sum) per split
   float *acc;
   int64_t acc_stride;
@@ -149,33 +152,24 @@ struct Misc {
   uint64_t q_full, done[2], never;
   uint32_t tmem_base, abort;
   __align__(16) float sig[kMaxQ];
+  __align__(16) float off[kMaxQ];
   __align__(16) float neg[kMaxQ];  // kAdd: -(log-sum-exp)
   float2 red[4][kMaxQ];            // kLse: per quarter of the lanes
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc block exceeds its reservation");
 
-// Eight codes -> four words of the score's A operand, in levels8's order.  BITS = 4
-// and 8: word k holds codes k and k + 4 (BITS = 8: 2k and 2k + 1) as subnormals,
-// times 2^(place_of(k) - 24).  BITS = 2: levels.  (The offset of two-bit codes is
-// large beside their scores, and the sums, truncated at its size, lose half a digit.)
-template <int BITS>
-__host__ __device__ constexpr int place_of(int k) {
-  return BITS == 4 ? 4 * (k & 1) : 0;
-}
-template <int BITS>
-__host__ __device__ constexpr int unit_of() {
-  return BITS == 2 ? 0 : 24;
-}
+// Eight codes -> four words of the score's A operand, in levels8's order.  BITS = 4:
+// word k holds codes k and k + 4 as subnormals, times 2^(place_of(k) - 24); else levels.
+constexpr bool raw_codes(int bits) { return bits == 4; }
+__host__ __device__ constexpr int place_of(int k) { return 4 * (k & 1); }
+__host__ __device__ constexpr int grid_bits(int G) { return 15 * G < 1 << 13 ? 10 : 9; }  // 15 G 2^(bits + 1) <= 2^24
 template <int BITS>
 __device__ __forceinline__ uint4 codes8(uint32_t w, uint32_t w2) {
-  if constexpr (BITS == 8) {
-    return make_uint4(__byte_perm(w, 0u, 0x4140), __byte_perm(w, 0u, 0x4342), __byte_perm(w2, 0u, 0x4140),
-                      __byte_perm(w2, 0u, 0x4342));
-  } else if constexpr (BITS == 4) {
+  if constexpr (raw_codes(BITS)) {
     const uint32_t v = w >> 8;
     return make_uint4(w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u);
   } else {
-    return levels8<2>(w, 0u);
+    return levels8<BITS>(w, w2);
   }
 }
 
@@ -269,7 +263,11 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
     tmem_alloc(&ms.tmem_base, 512);
     tmem_relinquish();
   }
-  if (tid < kMaxQ) ms.sig[tid] = tid < n_q ? p.sig[b * n_q + tid] : 0.f;
+  if (tid < kMaxQ) {
+    const float2 v = tid < n_q ? p.sig[b * n_q + tid] : make_float2(0.f, 0.f);
+    ms.sig[tid] = v.x;
+    ms.off[tid] = v.y;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -471,9 +469,11 @@ __global__ void __launch_bounds__(Shape<NC>::THREADS, 1) weights_split_tc(const 
         tmem_ld_wait16(x16);
         float2 x[4];  // S_hi + S_lo of two heads each
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = __fadd2_rn(make_float2(__uint_as_float(x16[2 * e]), __uint_as_float(x16[2 * e + 1])),
-                            make_float2(__uint_as_float(x16[8 + 2 * e]), __uint_as_float(x16[9 + 2 * e])));
+        for (int e = 0; e < 4; ++e) {
+          x[e] = make_float2(__uint_as_float(x16[2 * e]), __uint_as_float(x16[2 * e + 1]));
+          if constexpr (raw_codes(BITS)) x[e] = __fadd2_rn(x[e], *reinterpret_cast<const float2 *>(&ms.off[8 * ch + 2 * e]));
+          x[e] = __fadd2_rn(x[e], make_float2(__uint_as_float(x16[8 + 2 * e]), __uint_as_float(x16[9 + 2 * e])));
+        }
         if (c + 1 < CH) {
           fetch(i, c + 1, v[CH % 2 ? 0 : (c + 1) & 1]);
         } else {
@@ -586,7 +586,7 @@ template <int BITS>
 __global__ void __launch_bounds__(kAbsorbThreads, 1) weights_query(const uint16_t *__restrict__ q,
                                                                 const uint16_t *__restrict__ W_kv, int n_q, int n_kv,
                                                                 int G, int NA, int N, float c,
-                                                                uint8_t *__restrict__ qbuf, float *__restrict__ sig,
+                                                                uint8_t *__restrict__ qbuf, float2 *__restrict__ sig,
                                                                 uint32_t *err) {
   __shared__ AbsorbSmem<FSQ_MAX_G> sm;
   const int64_t b = blockIdx.y;
@@ -608,12 +608,18 @@ __global__ void __launch_bounds__(kAbsorbThreads, 1) weights_query(const uint16_
       sm, q, W_kv, n_q, n_kv, G, NA * kAtom, c, blockIdx.x, b,
       [&](int h, int g, float v, int e) {
         const int ph = (g & ~7) | order_of<BITS>(g & 7), n = (h >> 3) * 16 + (h & 7);
-        const float s = scalbnf(v, kTop - e - place_of<BITS>((ph & 7) / 2));
-        const __half hi = __float2half_rn(s);
-        *reinterpret_cast<__half *>(at(n, ph)) = hi;
-        *reinterpret_cast<__half *>(at(n + 8, ph)) = __float2half_rn(s - __half2float(hi));
+        float s = scalbnf(v, kTop - e), hi;
+        if constexpr (raw_codes(BITS)) hi = scalbnf(rintf(scalbnf(s, grid_bits(G) - kTop)), kTop - grid_bits(G));
+        else hi = __half2float(__float2half_rn(s));
+        const int place = raw_codes(BITS) ? place_of((ph & 7) / 2) : 0;
+        *reinterpret_cast<__half *>(at(n, ph)) = __float2half_rn(scalbnf(hi, -place));
+        *reinterpret_cast<__half *>(at(n + 8, ph)) = __float2half_rn(scalbnf(s - hi, -place));
+        return raw_codes(BITS) ? hi : 0.f;
       },
-      [&](int h, int e) { sig[b * n_q + h] = scalbnf(1.f, e - kTop + unit_of<BITS>()); });
+      [&](int h, int e, float sum) {
+        constexpr int unit = raw_codes(BITS) ? 24 : 0;
+        sig[b * n_q + h] = make_float2(scalbnf(1.f, e - kTop + unit), raw_codes(BITS) ? -scalbnf(sum, 3 - unit) : 0.f);
+      });
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -649,7 +655,7 @@ cudaError_t launch_nc(const CUtensorMap &map, const Params &p, int64_t B, const 
 
 template <int BITS>
 cudaError_t launch_t(const uint16_t *q, const uint16_t *W_kv, int n_kv, float scale, const Params &p, int64_t B,
-                     uint8_t *qbuf, float *sig, void *const *prof, cudaStream_t st) {
+                     uint8_t *qbuf, float2 *sig, void *const *prof, cudaStream_t st) {
   const Plan pl = plan_of(p.n_q, p.G, BITS);
   CUtensorMap map;
   memset(&map, 0, sizeof(map));
@@ -694,11 +700,11 @@ cudaError_t launch_weights(const uint16_t *q, int64_t B, int n_q, int n_kv, cons
                            int64_t T, const int32_t *seq_lens, int G, int bits, const uint16_t *W_kv, float scale, int S,
                            int k, float *acc, int64_t acc_stride, uint8_t *qbuf, float *sig, float *part, uint32_t *err,
                            uint32_t stall_ns, void *const *prof, cudaStream_t st) {
-  tc::weights::Params p{codes, bstride, T, seq_lens, qbuf, sig, (float2 *)part, acc, acc_stride, err,
+  tc::weights::Params p{codes, bstride, T, seq_lens, qbuf, (float2 *)sig, (float2 *)part, acc, acc_stride, err,
                         n_q, G, S, k, stall_ns};
-  return bits == 2   ? tc::weights::launch_t<2>(q, W_kv, n_kv, scale, p, B, qbuf, sig, prof, st)
-         : bits == 4 ? tc::weights::launch_t<4>(q, W_kv, n_kv, scale, p, B, qbuf, sig, prof, st)
-                     : tc::weights::launch_t<8>(q, W_kv, n_kv, scale, p, B, qbuf, sig, prof, st);
+  return bits == 2   ? tc::weights::launch_t<2>(q, W_kv, n_kv, scale, p, B, qbuf, (float2 *)sig, prof, st)
+         : bits == 4 ? tc::weights::launch_t<4>(q, W_kv, n_kv, scale, p, B, qbuf, (float2 *)sig, prof, st)
+                     : tc::weights::launch_t<8>(q, W_kv, n_kv, scale, p, B, qbuf, (float2 *)sig, prof, st);
 }
 
 }  // namespace fsq

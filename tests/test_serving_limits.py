@@ -134,6 +134,47 @@ def test_prefix_holds_sharp_scores(q_scale, G, L):
             assert (np.abs(got[b, h] - o) <= tol).all(), (b, h, (np.abs(got[b, h] - o) / tol).max())
 
 
+# ---------------------------------------------------------------- attention weights: a common component of W_k
+@pytest.mark.parametrize("G,L,spread", [(256, 16, 0), (84, 16, 0), (576, 16, 6), (144, 256, 0), (256, 256, 0), (320, 4, 0)])
+def test_weights_under_a_common_component(G, L, spread):
+    """W_k with a component that all coordinates share (up to 2^-spread of it, alike in
+    a pair), on latents whose coordinates cancel in pairs: it leaves the scores
+    alone, but sum_g q'_g is large.
+
+    A score's products are at most max|q'| max|z| and its partial sums that and
+    max|s|: together M, to which each of its Gp / 16 steps truncates products
+    and sum, 2^-23 M each.  The queries' own roundings (22 bits, fp32 sums of 128)
+    are independent over the coordinates, of spread 1.3 2^-24 |q'_g| each: six
+    times that over all of them.  The log-sum-exp carries the same once more."""
+    T = 3000
+    r = np.random.default_rng(G + L)
+    top = L // 2 - 1
+    z = np.empty((T, G), np.int64)
+    z[:, ::2] = np.clip(np.round(r.normal(size=(T, G // 2)) * 0.58 * L / 2), -top, top)
+    z[:, 1::2] = -z[:, ::2]
+    codes = np.zeros((1, (T + 15) // 16 * 16, F.row_bytes(G, L)), np.uint8)
+    codes[0, :T] = O.pack(z, L)
+    W, q = decoder_weights(1, 1, G, 1, 13, levels=L)
+    common = torch.from_numpy(8.0 * 16 / L * 2.0 ** -(spread * r.random(G // 2).repeat(2))).float()
+    W[:128] = (W[:128].float() + common).to(torch.bfloat16)
+    q = q.abs()
+    acc, ws = torch.zeros((1, T), device=DEV), F.Workspace()
+    F.attn_weights(_dev(q), _dev(codes), _dev(W), acc, T, 1, G, opts=F.attn_opts(levels=L), workspace=ws)
+    assert F.workspace_status(ws.buf) == F.FSQ_OK
+    qa = W[:128].double().numpy().T @ q[0, 0].double().numpy() / math.sqrt(128) * LOG2E
+    s = z @ qa
+    want = O.softmax(s * math.log(2))
+    big = np.abs(qa).max()
+    M = big * np.abs(z).max() + np.abs(s).max()
+    trunc = (G + 15) // 16 * 2.0 ** -22 * M
+    rounding = 6 * math.sqrt((z * z).mean() * (qa * qa).sum()) * 1.3 * 2.0 ** -24
+    got = acc[0].double().cpu().numpy()
+    live = want > 1e-30
+    worst = (np.abs(got - want)[live] / want[live]).max()
+    assert worst <= 2 * math.log(2) * (trunc + rounding), worst
+    assert (got[~live] <= 2e-30).all()
+
+
 # ---------------------------------------------------------------- eviction: rows that stay whole, in clusters
 @pytest.mark.parametrize("B,T", [(300, 5000), (300, 20001), (150, 70000)])
 @pytest.mark.parametrize("recent", ["some", "all"])

@@ -471,11 +471,6 @@ def _vector(t, n, dtype, what):
         raise ValueError(f"{what} must hold {n} contiguous {dtype} values")
 
 
-def _of_type(t, dtype, what):
-    if t is not None and t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}")
-
-
 def qk_norm_rope(q, k=None, q_gain=None, k_gain=None, positions=None, pos0=0, eps=1e-6, rope_base=1.0e6,
                  q_out=None, k_out=None, stream=None):
     """RMS norm of every query (and key) head, then its rotary position, in one

@@ -448,6 +448,14 @@ def _launch(what, stream, *tensors):
     return torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream() without the Stream object
 
 
+def _scratch(what, workspace, like, nbytes):
+    """A call's workspace: on the tensors' device, which a caller's need not be."""
+    ws = (workspace or Workspace(like.device)).get(nbytes)
+    if ws.get_device() != like.get_device():
+        raise ValueError(f"{what}: the workspace must be on the tensors' device, got {ws.device}")
+    return ws
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -571,7 +579,7 @@ def decode_attn_prefix(q, prefix, codes, W_kv, T_prefix, T, n_kv, G, opts=None, 
         raise ValueError(f"out must be contiguous [B, n_q, d_h] {dtype}")
     s = _launch("decode_attn_prefix", stream, q, prefix, codes, W_kv, out, lens)
     with _on(stream):
-        ws = (workspace or Workspace(q.device)).get(prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
+        ws = _scratch("decode_attn_prefix", workspace, q, prefix_workspace_size(B, T_prefix, T, n_q, n_kv, d_h, G, opts))
     st = decode_attn_prefix_raw(q.data_ptr(), B, n_q, d_h, prefix.data_ptr(), T_prefix, _opt_ptr(codes), stride, T, G,
                                 W_kv.data_ptr(), n_kv, opts, ws.data_ptr(), ws.numel(), out.data_ptr(), s)
     _check(st, "fsq_decode_attn_prefix")
@@ -587,7 +595,7 @@ def attn_weights(q, codes, W_kv, acc, T, n_kv, G, opts=None, workspace=None, str
     cs, as_ = _cache_stride(codes, rb, B, T, "codes"), _acc_stride(acc, B, T, "acc")
     s = _launch("attn_weights", stream, q, codes, W_kv, acc, lens)
     with _on(stream):
-        ws = (workspace or Workspace(q.device)).get(attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
+        ws = _scratch("attn_weights", workspace, q, attn_weights_workspace_size(B, T, n_q, n_kv, d_h, G, opts))
     st = attn_weights_raw(q.data_ptr(), B, n_q, d_h, codes.data_ptr(), cs, T, G, W_kv.data_ptr(), n_kv, opts,
                           acc.data_ptr(), as_, ws.data_ptr(), ws.numel(), s)
     _check(st, "fsq_attn_weights")
@@ -620,7 +628,7 @@ def cache_evict(codes, acc, T, n_keep, n_recent=0, G=256, levels=16, seq_lens=No
     if nbytes == 0:
         raise FsqError(FSQ_ERR_INVALID_ARG, "fsq_cache_evict_workspace_size")
     with _on(stream):
-        ws = (workspace or Workspace(codes.device)).get(nbytes)
+        ws = _scratch("cache_evict", workspace, codes, nbytes)
     st = _lib().fsq_cache_evict(codes.data_ptr(), cs, acc.data_ptr(), as_, _opt_ptr(seq_lens), B, T, n_keep, n_recent, G,
                                 levels, out.data_ptr(), os_, acc_out.data_ptr(), aos, _opt_ptr(lens_out),
                                 _opt_ptr(kept), ws.data_ptr(), ws.numel(), s)

@@ -169,3 +169,10 @@ def test_a_call_runs_on_the_current_device_alone(monkeypatch):
         (ELSEWHERE, lambda: _abi._launch("op", None, _On(-1))),          # none
         ("the stream must be on the tensors' device", lambda: _abi._launch("op", _On(0), _On(1))),
     ])
+
+
+def test_a_workspace_of_another_device_is_refused():
+    from fsq_latent_decode_b200 import _abi
+    assert _abi._scratch("op", None, torch.zeros(1), 1000).numel() == 1000
+    with pytest.raises(ValueError, match="op: the workspace must be on the tensors' device, got cpu"):
+        _abi._scratch("op", F.Workspace("cpu"), _On(1), 1000)

@@ -355,16 +355,26 @@ def quantize_pack_f32(u, h=None, delta=0.5, out=None, stream=None, levels=16):
 
 
 class Workspace:
-    """Caller-owned device workspace, grown on demand (torch allocates it)."""
+    """Caller-owned device workspace, grown on demand (torch allocates it).  Calls
+    that may run at the same time need one each.  A buffer that a CUDA graph was
+    captured with lives as long as the workspace does: outgrown, it is kept for the
+    graph's replays."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self._captured = False  # whether a graph holds buf
+        self._held = []         # outgrown buffers that graphs hold
 
     def get(self, nbytes: int):
         import torch
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._held.append(self.buf)
+                self._captured = False
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        if not self._captured and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self.buf
 
 

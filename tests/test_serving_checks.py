@@ -176,3 +176,23 @@ def test_a_workspace_of_another_device_is_refused():
     assert _abi._scratch("op", None, torch.zeros(1), 1000).numel() == 1000
     with pytest.raises(ValueError, match="op: the workspace must be on the tensors' device, got cpu"):
         _abi._scratch("op", F.Workspace("cpu"), _On(1), 1000)
+
+
+def test_a_workspace_keeps_what_a_graph_was_captured_with(monkeypatch):
+    ws, capturing = F.Workspace("cpu"), False
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    import weakref
+    first = weakref.ref(ws.get(1000))
+    assert ws.get(900) is first()
+    second = weakref.ref(ws.get(2000))
+    assert first() is None  # no graph: an outgrown buffer goes
+    capturing = True
+    assert ws.get(500) is second()
+    capturing = False
+    third = weakref.ref(ws.get(5000))
+    assert second() is not None and third() is not second()
+    ws.get(9000)
+    assert second() is not None and third() is None
+    del ws
+    assert second() is None

@@ -201,3 +201,26 @@ def test_evict_of_rows_without_a_choice(B, T, recent):
         for b, at in enumerate(want):
             assert np.array_equal(got[b, :len(at)], at) and (got[b, len(at):] == -1).all()
             assert np.array_equal(gc[b, :len(at)], codes[b, at]) and np.array_equal(ga[b, :len(at)], acc[b, at])
+
+
+# ---------------------------------------------------------------- a graph and a workspace that grows
+def test_a_graph_replays_in_the_workspace_it_was_captured_with():
+    """After a capture the same workspace grows for a longer call: the graph's buffer is
+    not handed out to tensors made since."""
+    G, T = 84, 300
+    codes = oracle_cache(2, T, G, 621)
+    W, q = decoder_weights(16, 8, G, 2, 622)
+    a, ws = (_dev(q), _dev(codes), _dev(W)), F.Workspace()
+    acc = torch.zeros((2, T), device=DEV)
+    want = F.attn_weights(*a, torch.zeros_like(acc), T, 8, G, workspace=ws).clone()
+    old, size = ws.buf.data_ptr(), ws.buf.numel()
+    g, o = torch.cuda.CUDAGraph(), F.attn_opts()
+    with torch.cuda.graph(g):
+        F.attn_weights(*a, acc, T, 8, G, opts=o, workspace=ws)
+    acc.zero_()
+    ws.get(4 * size)
+    assert ws.buf.data_ptr() != old
+    fill = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(40)]
+    assert all(f.data_ptr() != old for f in fill)
+    g.replay()
+    assert torch.equal(acc, want) and all((f == 7).all() for f in fill)

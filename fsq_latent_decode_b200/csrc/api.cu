@@ -661,6 +661,12 @@ fsq_status fsq_cache_evict(const uint8_t *codes, int64_t code_batch_stride_bytes
       (overlap(codes, (B - 1) * code_batch_stride_bytes + T * R, codes_out, (B - 1) * out_stride_bytes + rows_out * R) ||
        overlap(acc, ((B - 1) * acc_stride + T) * 4, acc_out, ((B - 1) * acc_out_stride + rows_out) * 4)))
     return FSQ_ERR_INVALID_ARG;
+  // lengths and indices: rows read their length and write the new one at different times
+  const int64_t len_bytes = 4 * B, kept_bytes = n_keep > INT64_MAX / 4 / B ? INT64_MAX : 4 * B * n_keep;
+  if ((seq_lens && lens_out && seq_lens != lens_out && overlap(seq_lens, len_bytes, lens_out, len_bytes)) ||
+      (kept && seq_lens && overlap(kept, kept_bytes, seq_lens, len_bytes)) ||
+      (kept && lens_out && overlap(kept, kept_bytes, lens_out, len_bytes)))
+    return FSQ_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < evict_workspace_bytes(B, T, (int)R)) return FSQ_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255u) return FSQ_ERR_MISALIGNED;
   return from_cuda(launch_evict(codes, code_batch_stride_bytes, acc, acc_stride, seq_lens, B, T, n_keep, n_recent,

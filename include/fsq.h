@@ -377,6 +377,7 @@ FSQ_API fsq_status fsq_qk_norm_rope(const uint16_t *q, int64_t ldq, int n_q, con
  *             seq_lens                                                 — written
  *  kept       device int32 [B, n_keep], the kept tokens' old indices, ascending,
  *             -1 behind the last, or NULL                              — written
+ *  Of seq_lens, lens_out and kept no two may overlap, but lens_out be seq_lens.
  *  workspace  >= fsq_cache_evict_workspace_size(...) bytes, 256-byte aligned; its
  *             error word is read with fsq_workspace_status
  * In place, a part of a row waits until the parts that it moves onto are read.  The

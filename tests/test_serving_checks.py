@@ -196,3 +196,18 @@ def test_a_workspace_keeps_what_a_graph_was_captured_with(monkeypatch):
     assert second() is not None and third() is None
     del ws
     assert second() is None
+
+
+def test_evict_refuses_lengths_and_indices_that_overlap():
+    """Rows read their length and write the new one at different times: the two arrays
+    are one, or apart; so are the kept indices."""
+    def call(lens=None, lens_out=None, kept=None, keep=60, recent=5):
+        return F.cache_evict_raw(1 << 20, 12800, 2 << 20, 100, lens, 3, 100, keep, recent, 256, 16, 3 << 20, 7680, 4 << 20,
+                                 60, lens_out, kept, None, 0, None)
+
+    bad, ok = F.FSQ_ERR_INVALID_ARG, F.FSQ_ERR_WORKSPACE  # past the checks: no workspace
+    m = 6 << 20
+    assert call(m, m) == call(m, m + 12) == call(m, None, m + 12) == call(m, m, m + 12) == call(None, m, m + 12) == ok
+    assert call(m, m + 4) == call(m + 8, m) == bad
+    assert call(m, None, m) == call(m, None, m - 716) == call(None, m, m - 4) == call(m, m + 12, m + 20) == bad
+    assert call(m, None, m - 720) == ok

@@ -22,7 +22,8 @@
 // chunks it overwrites have published the same, and stores.  Chunks are taken in
 // ascending order from a counter, and a chunk publishes before it waits, so the
 // chunks waited for are always running or done: the wait ends whatever the
-// scheduling.  It is bounded all the same (FSQ_ERR_TIMEOUT).
+// scheduling.  It is bounded all the same (FSQ_ERR_TIMEOUT; the row is then left as it is,
+// part moved).
 //
 // Measured, 16 rows of 131072 tokens cut to 65536, 128-byte rows: select 34 us,
 // compaction 56 us (277 MB: 5.0 TB/s); one row of 2048: 7.2 and 2.9 us.  The select
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kCopyNT, 4) evict_compact(CopyParams p) {
   uint4 v[U == 16 ? kRegs : 1];
   if constexpr (U == 16) {
     const int ppr = p.R / 16;       // pieces per row
-    const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 2048 (kCopyBytes / 16)
+    const uint32_t inv = (65536u + ppr - 1) / ppr;  // x / ppr for x < 2048 (kCopyBytes / 16) and ppr <= 50; rows end at 36
 #pragma unroll
     for (int k = 0; k < kRegs; ++k) {
       if (k * kCopyNT >= n * ppr) break;  // uniform: no index arithmetic for rows that go

@@ -13,6 +13,8 @@
 // p * (base^(-2i/128) / 2 pi) in 64 bits: without its whole turns the rest goes to
 // sincospif, so a far position loses nothing to the range reduction.  The first
 // heads are loaded before the angles are formed, the next before these are stored.
+// The kernel may not let its dependents start early: the attention kernels behind
+// it read the q that it writes before their own wait.
 // Measured: 61 us for 16383 tokens of 40 heads read out of a fused projection (336
 // MB: 5.5 TB/s, 84 % of the measured copy); one token of 40 heads 1.8 us.
 #include <math.h>

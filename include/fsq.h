@@ -288,7 +288,7 @@ FSQ_API const char *fsq_decode_attn_kernel(int64_t B, int n_new, int64_t T, int 
  * records FSQ_ERR_INVALID_ARG in the error word).  The result is that of
  * fsq_decode_attn on the concatenated rows.
  *  prefix_codes  uint8 [T_prefix] rows of R bytes, 16-byte aligned        — read
- *  codes         as in fsq_decode_attn; not looked at when T == 0         — read
+ *  codes         as in fsq_decode_attn; not looked at when T == 0 (nor the lengths) — read
  *  q, W_kv, o, opts, workspace (fsq_decode_attn_prefix_workspace_size): as in
  *  fsq_decode_attn, except that q is read after the kernels before it; the
  *  form is the absorbed one (variant AUTO or ABSORBED, rope_knorm 0; others

@@ -211,3 +211,9 @@ def test_evict_refuses_lengths_and_indices_that_overlap():
     assert call(m, m + 4) == call(m + 8, m) == bad
     assert call(m, None, m) == call(m, None, m - 716) == call(None, m, m - 4) == call(m, m + 12, m + 20) == bad
     assert call(m, None, m - 720) == ok
+
+
+def test_prefix_splits_hold_2_to_22_tokens_at_most():
+    one = F.attn_opts(num_splits=1)
+    size = lambda Tp: F.prefix_workspace_size(1, Tp, 0, 8, 2, 128, 64, one)  # noqa: E731
+    assert size(1) == size(1 << 22) < size((1 << 22) + 1) == size(1 << 23) < size((1 << 23) + 1)

@@ -317,10 +317,10 @@ FSQ_API fsq_status fsq_decode_attn_prefix(const uint16_t *q, int64_t B, int n_q,
  *  fsq_decode_attn, except that q is read after the kernels before it and W_v is
  *  not read; keys are W_k z_t (variant AUTO or ABSORBED, rope_knorm 0; others
  *  return FSQ_ERR_UNSUPPORTED), out_fp32 is not looked at.
- * Scores are sums in fp32 over the signed levels of Q' in 22 bits (21 at G > 546); W_k
- * may have a component that all coordinates share.  A call whose first
- * pass gives up a bounded wait (FSQ_ERR_TIMEOUT) adds nothing; one that gives up
- * later leaves acc undefined.
+ * Scores are fp32 sums of Q' (22 bits, 21 at G > 546) times the signed levels, at the
+ * size of those products: a component that W_k's coordinates share costs nothing.  A
+ * call whose first pass gives up a bounded wait (FSQ_ERR_TIMEOUT) adds nothing; one
+ * that gives up later leaves acc undefined.
  * Needs: d_h == 128, n_q % n_kv == 0, n_q <= 64, the G rules of the append, acc
  * 4-byte aligned, acc_stride >= T, T >= 1, T * R <= 2^37, B <= 65535.  B == 0 is
  * a no-op. */
